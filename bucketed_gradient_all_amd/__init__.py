@@ -1,5 +1,6 @@
 """Python binding of libddp.so (include/ddp.h): bucketed gradient reduction
-for data-parallel training on MI355X (gfx950).
+for data-parallel training on MI355X (gfx950), the norm and clipping of the
+gradients, and the embedding's lookup and gradient.
 
 Argument marshalling only: every step of the path runs in the C++ host
 library and its HIP kernels. The functions keep the C names; a negative
@@ -46,13 +47,25 @@ DDP_IN_F32_COPY = 0
 DDP_IN_F32_VIEW = 1
 DDP_IN_BF16_ACCUM_F32 = 2
 
+DDP_F32 = 0
+DDP_BF16 = 1
+DDP_F16 = 2
+
+DDP_NORM_INF = 0
+DDP_NORM_L1 = 1
+DDP_NORM_L2 = 2
+
+DDP_I32 = 0
+DDP_I64 = 1
+
 HIPCC_FLAGS = ["--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17",
                "-ffp-contract=off", "-fno-fast-math",
                "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 
 # one object per source; the kernel families compile in parallel
-SOURCES = ["reducer.cpp", "bucket_reduce.hip", "bucket_bf16_hook.hip", "bucket_fp16_hook.hip", "static_tables.hip"]
-HEADERS = ["internal.h", "reduce_kernels.h", "static_area.h"]
+SOURCES = ["reducer.cpp", "grad_list.cpp", "embedding.cpp", "bucket_reduce.hip", "bucket_bf16_hook.hip",
+           "bucket_fp16_hook.hip", "static_tables.hip", "grad_norm.hip", "embedding.hip"]
+HEADERS = ["host_common.h", "internal.h", "reduce_kernels.h", "static_area.h", "grad_list.h", "embedding.h"]
 
 
 BUILD_DIR = os.path.join(HERE, "_build")
@@ -126,6 +139,37 @@ class ddp_reducer_desc(ctypes.Structure):
     ]
 
 
+class ddp_grads_desc(ctypes.Structure):
+    _fields_ = [
+        ("n_tensors", ctypes.c_int32),
+        ("n_copies", ctypes.c_int32),
+        ("numel", ctypes.c_void_p),
+        ("dtype", ctypes.c_void_p),
+        ("grads", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("out_dtype", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class ddp_embedding_desc(ctypes.Structure):
+    _fields_ = [
+        ("n_rows", ctypes.c_int64),
+        ("width", ctypes.c_int64),
+        ("first_row", ctypes.c_int64),
+        ("padding_idx", ctypes.c_int64),
+        ("table_stride", ctypes.c_int64),
+        ("grad_stride", ctypes.c_int64),
+        ("act_stride", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("index_dtype", ctypes.c_int32),
+        ("table_dtype", ctypes.c_int32),
+        ("grad_dtype", ctypes.c_int32),
+        ("act_dtype", ctypes.c_int32),
+    ]
+
+
 _lib = None
 
 
@@ -136,7 +180,7 @@ def lib():
             raise RuntimeError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
                                "(there is no fallback path)")
         L = ctypes.CDLL(LIB_PATH)
-        P, I32, I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+        P, I32, I64, F32, SIZE = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
         sig = {
             "ddp_plan_buckets": [I32, P, P, I32, I64, I64, P, P, P, P, P, P],
             "ddp_reducer_create": [ctypes.POINTER(ddp_reducer_desc), ctypes.POINTER(ctypes.c_void_p)],
@@ -160,13 +204,27 @@ def lib():
             "ddp_set_bucket_groups": [P, P, I32],
             "ddp_set_workgroups_per_cu": [P, I32],
             "ddp_get_launch_lds": [P, P],
+            "ddp_grads_create": [ctypes.POINTER(ddp_grads_desc), ctypes.POINTER(ctypes.c_void_p)],
+            "ddp_grads_from_reducer": [P, P, SIZE, ctypes.POINTER(ctypes.c_void_p)],
+            "ddp_grads_destroy": [P],
+            "ddp_grads_scratch_bytes": [P, P],
+            "ddp_grad_norm": [P, I32, P, P, SIZE, P],
+            "ddp_clip_grad_norm": [P, I32, F32, P, P, SIZE, P],
+            "ddp_clip_grads": [P, F32, P, P],
+            "ddp_embedding_lookup": [ctypes.POINTER(ddp_embedding_desc), P, P, I64, P, P],
+            "ddp_embedding_grad": [ctypes.POINTER(ddp_embedding_desc), P, P, I64, P, I32, P, SIZE, P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
             f.argtypes = args
             f.restype = ctypes.c_int
-        L.ddp_workspace_bytes.argtypes = [ctypes.POINTER(ddp_reducer_desc)]
-        L.ddp_workspace_bytes.restype = ctypes.c_size_t
+        for name, args in {"ddp_workspace_bytes": [ctypes.POINTER(ddp_reducer_desc)],
+                           "ddp_grads_workspace_bytes": [ctypes.POINTER(ddp_grads_desc)],
+                           "ddp_reducer_grads_workspace_bytes": [P],
+                           "ddp_embedding_grad_workspace_bytes": [ctypes.POINTER(ddp_embedding_desc), I64]}.items():
+            f = getattr(L, name)
+            f.argtypes = args
+            f.restype = ctypes.c_size_t
         L.ddp_last_error.argtypes = []
         L.ddp_last_error.restype = ctypes.c_char_p
         _lib = L
@@ -505,3 +563,192 @@ def make_reducer(world: int, param_numel: Sequence[int], plan: BucketPlan, input
     r.workspace = ws
     r.keep_alive(ws)   # released only after the native reducer, which waits for its reductions
     return r
+
+
+class GradsDesc:
+    """Owns the host arrays a ddp_grads_desc points to. grad_ptrs and out_ptrs:
+    one list of device pointers per copy; dtype and out_dtype: DDP_F32 /
+    DDP_BF16 / DDP_F16 per tensor (None: fp32, and as dtype)."""
+
+    def __init__(self, numel: Sequence[int], grad_ptrs: Sequence[Sequence[int]],
+                 dtype: Optional[Sequence[int]] = None, out_ptrs: Optional[Sequence[Sequence[int]]] = None,
+                 out_dtype: Optional[Sequence[int]] = None, workspace: int = 0, workspace_bytes: int = 0):
+        self.numel = np.ascontiguousarray(numel, dtype=np.int64).reshape(-1)
+        N, R = self.numel.size, len(grad_ptrs)
+
+        def pointers(what, v):
+            a = np.asarray([list(c) for c in v], dtype=np.uint64).reshape(-1)
+            if a.size != R * N or len(v) != R:
+                raise ValueError(f"{what} needs {R} copies of {N} pointers")
+            return np.ascontiguousarray(a)
+
+        def types(what, v):
+            a = np.ascontiguousarray(v, dtype=np.int32).reshape(-1)
+            if a.size != N:
+                raise ValueError(f"{what} needs {N} entries, got {a.size}")
+            return a
+
+        self.grads = pointers("grad_ptrs", grad_ptrs)
+        self.out = pointers("out_ptrs", out_ptrs) if out_ptrs is not None else None
+        self.dtype = types("dtype", dtype) if dtype is not None else None
+        self.out_dtype = types("out_dtype", out_dtype) if out_dtype is not None else None
+        d = ddp_grads_desc()
+        d.n_tensors, d.n_copies = N, R
+        d.numel = self.numel.ctypes.data
+        d.grads = self.grads.ctypes.data
+        d.dtype = self.dtype.ctypes.data if self.dtype is not None else None
+        d.out = self.out.ctypes.data if self.out is not None else None
+        d.out_dtype = self.out_dtype.ctypes.data if self.out_dtype is not None else None
+        d.workspace, d.workspace_bytes = workspace or None, workspace_bytes
+        self.c = d
+
+    def set_workspace(self, ptr: int, nbytes: int) -> None:
+        self.c.workspace = ptr or None
+        self.c.workspace_bytes = nbytes
+
+
+def ddp_grads_workspace_bytes(desc: GradsDesc) -> int:
+    n = lib().ddp_grads_workspace_bytes(ctypes.byref(desc.c))
+    if n == 0:
+        raise DDPError(DDP_ERR_INVALID, ddp_last_error())
+    return int(n)
+
+
+def _release_grads(holder: list, L) -> None:
+    h, holder[0] = holder[0], None
+    if h:
+        L.ddp_grads_destroy(h)
+
+
+class Grads:
+    """Handle of a ddp_grads, and the scratch its calls use by default."""
+
+    def __init__(self, handle: int):
+        self._holder = [handle]
+        self._lib = lib()
+        self._finalizer = weakref.finalize(self, _release_grads, self._holder, self._lib)
+        self.workspace = None                 # device allocations that live as long as the handle
+        self.scratch = None
+        self._scratch = (None, 0)
+
+    @property
+    def handle(self):
+        return self._holder[0]
+
+    def set_scratch(self, ptr: int, nbytes: int) -> None:
+        """The scratch of calls that are given none."""
+        self._scratch = (ptr or None, nbytes)
+
+
+def ddp_grads_create(desc: GradsDesc) -> Grads:
+    h = ctypes.c_void_p()
+    _check(lib().ddp_grads_create(ctypes.byref(desc.c), ctypes.byref(h)))
+    return Grads(h.value)
+
+
+def ddp_reducer_grads_workspace_bytes(r: Reducer) -> int:
+    n = r._lib.ddp_reducer_grads_workspace_bytes(r.handle)
+    if n == 0:
+        raise DDPError(DDP_ERR_INVALID, r._lib.ddp_last_error().decode())
+    return int(n)
+
+
+def ddp_grads_from_reducer(r: Reducer, workspace: int, workspace_bytes: int) -> Grads:
+    h = ctypes.c_void_p()
+    _check(r._lib.ddp_grads_from_reducer(r.handle, workspace or None, workspace_bytes, ctypes.byref(h)), r._lib)
+    return Grads(h.value)
+
+
+def ddp_grads_destroy(g: Grads) -> None:
+    g._finalizer.detach()
+    _release_grads(g._holder, g._lib)
+
+
+def ddp_grads_scratch_bytes(g: Grads) -> int:
+    n = ctypes.c_size_t()
+    _check(g._lib.ddp_grads_scratch_bytes(g.handle, ctypes.byref(n)), g._lib)
+    return n.value
+
+
+def ddp_grad_norm(g: Grads, norm_type: int, norm: int, stream: int, scratch: int = 0, scratch_bytes: int = 0) -> None:
+    """norm: device pointer of one float. Without a scratch the handle's own
+    is used: then no other call of the handle may run at the same time."""
+    p, n = (scratch, scratch_bytes) if scratch else g._scratch
+    _check(g._lib.ddp_grad_norm(g.handle, norm_type, norm or None, p, n, stream or None), g._lib)
+
+
+def ddp_clip_grad_norm(g: Grads, norm_type: int, max_norm: float, norm: int, stream: int, scratch: int = 0,
+                       scratch_bytes: int = 0) -> None:
+    p, n = (scratch, scratch_bytes) if scratch else g._scratch
+    _check(g._lib.ddp_clip_grad_norm(g.handle, norm_type, max_norm, norm or None, p, n, stream or None), g._lib)
+
+
+def ddp_clip_grads(g: Grads, max_norm: float, norm: int, stream: int) -> None:
+    _check(g._lib.ddp_clip_grads(g.handle, max_norm, norm or None, stream or None), g._lib)
+
+
+def _with_scratch(g: Grads, ws) -> Grads:
+    import torch
+    g.workspace = ws
+    n = ddp_grads_scratch_bytes(g)
+    g.scratch = torch.empty(n, dtype=torch.uint8, device=ws.device)
+    g.set_scratch(g.scratch.data_ptr(), n)
+    return g
+
+
+def make_grads(numel: Sequence[int], grad_ptrs: Sequence[Sequence[int]], dtype: Optional[Sequence[int]] = None,
+               out_ptrs: Optional[Sequence[Sequence[int]]] = None,
+               out_dtype: Optional[Sequence[int]] = None) -> Grads:
+    """Creates a gradient list on the current device; its workspace and a
+    scratch are torch allocations that the returned handle keeps alive."""
+    import torch
+
+    desc = GradsDesc(numel, grad_ptrs, dtype, out_ptrs, out_dtype)
+    nbytes = ddp_grads_workspace_bytes(desc)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    desc.set_workspace(ws.data_ptr(), nbytes)
+    return _with_scratch(ddp_grads_create(desc), ws)
+
+
+def make_reducer_grads(r: Reducer) -> Grads:
+    """make_grads over a reducer's results (ddp_grads_from_reducer)."""
+    import torch
+
+    nbytes = ddp_reducer_grads_workspace_bytes(r)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    return _with_scratch(ddp_grads_from_reducer(r, ws.data_ptr(), nbytes), ws)
+
+
+class EmbeddingDesc:
+    """A ddp_embedding_desc; strides default to the width."""
+
+    def __init__(self, n_rows: int, width: int, table_dtype: int = DDP_F32, grad_dtype: int = DDP_F32,
+                 act_dtype: int = DDP_F32, index_dtype: int = DDP_I64, scale: float = 1.0, first_row: int = 0,
+                 padding_idx: int = -1, table_stride: Optional[int] = None, grad_stride: Optional[int] = None,
+                 act_stride: Optional[int] = None):
+        d = ddp_embedding_desc()
+        d.n_rows, d.width, d.first_row, d.padding_idx = n_rows, width, first_row, padding_idx
+        d.table_stride = width if table_stride is None else table_stride
+        d.grad_stride = width if grad_stride is None else grad_stride
+        d.act_stride = width if act_stride is None else act_stride
+        d.scale = scale
+        d.index_dtype, d.table_dtype, d.grad_dtype, d.act_dtype = index_dtype, table_dtype, grad_dtype, act_dtype
+        self.c = d
+
+
+def ddp_embedding_lookup(desc: EmbeddingDesc, table: int, tokens: int, n_tokens: int, out: int, stream: int) -> None:
+    _check(lib().ddp_embedding_lookup(ctypes.byref(desc.c), table or None, tokens or None, n_tokens, out or None,
+                                      stream or None))
+
+
+def ddp_embedding_grad_workspace_bytes(desc: EmbeddingDesc, n_tokens: int) -> int:
+    n = lib().ddp_embedding_grad_workspace_bytes(ctypes.byref(desc.c), n_tokens)
+    if n == 0:
+        raise DDPError(DDP_ERR_INVALID, ddp_last_error())
+    return int(n)
+
+
+def ddp_embedding_grad(desc: EmbeddingDesc, dout: int, tokens: int, n_tokens: int, grad: int, accumulate: bool,
+                       workspace: int, workspace_bytes: int, stream: int) -> None:
+    _check(lib().ddp_embedding_grad(ctypes.byref(desc.c), dout or None, tokens or None, n_tokens, grad or None,
+                                    1 if accumulate else 0, workspace or None, workspace_bytes, stream or None))

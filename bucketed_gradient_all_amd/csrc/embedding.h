@@ -1,0 +1,47 @@
+// Internal types shared by the host half of the embedding operators
+// (embedding.cpp) and their kernels (embedding.hip). Not part of the C ABI.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+
+#include <cstdint>
+
+namespace ddp {
+
+constexpr int kSortThreads = 1024;             // 16 waves
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kMaxSortRows = 2048;             // rows of one sorting workgroup: 128 KiB of LDS counters
+
+// Sorted positions one wave sums (a chunk), at most.
+constexpr int kMaxChunk = 64;
+
+struct EmbeddingArgs {
+    int64_t n_rows, width;
+    int64_t first_row, padding_idx;
+    int64_t table_stride, grad_stride, act_stride;
+    int64_t n_tokens;
+    float scale;
+    int32_t index64;
+    int32_t table_dtype, grad_dtype, act_dtype;
+};
+
+// The gradient's workspace.
+struct EmbeddingWork {
+    int32_t *row;     // [T] rows of the sorted positions
+    int32_t *pos;     // [T] the positions, sorted by row, then by position
+    int32_t *begin;   // [V + 1] where each row's positions begin; the last: how many there are
+    float *first;     // [chunks][slots] sums of the pieces that begin a long run
+    float *more;      // [chunks][slots] sums of the pieces that go on with one
+    int64_t pitch;    // elements of one chunk's slot: the width rounded up
+    int32_t chunk;    // positions of a chunk
+    int32_t n_chunks;
+    int32_t sort_rows;   // rows of one sorting workgroup
+};
+
+hipError_t launch_lookup(const EmbeddingArgs &a, const void *table, const void *tokens, void *out, hipStream_t s);
+hipError_t launch_sort(const EmbeddingArgs &a, const void *tokens, const EmbeddingWork &w, hipStream_t s);
+hipError_t launch_sum(const EmbeddingArgs &a, const void *dout, void *grad, bool accumulate, const EmbeddingWork &w,
+                      hipStream_t s);
+hipError_t launch_join(const EmbeddingArgs &a, void *grad, bool accumulate, const EmbeddingWork &w, hipStream_t s);
+
+}  // namespace ddp

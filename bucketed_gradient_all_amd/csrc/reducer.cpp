@@ -3,6 +3,7 @@
 //
 // Sources are cited by tag and section; the tags are defined in include/ddp.h.
 #include "../../include/ddp.h"
+#include "host_common.h"
 #include "internal.h"
 #include "static_area.h"
 
@@ -28,6 +29,10 @@ namespace {
 thread_local std::string g_err;
 thread_local const char *g_err_fixed = nullptr;
 constexpr const char *kNoMemText = "out of host memory";
+
+}  // namespace
+
+namespace ddp {
 
 int fail(int code, const std::string &msg) noexcept
 {
@@ -64,6 +69,19 @@ int hip_fail(const char *what, hipError_t e) noexcept
     return DDP_ERR_HIP;
 }
 
+int no_memory() noexcept
+{
+    return fail(DDP_ERR_NOMEM, kNoMemText);
+}
+
+}  // namespace ddp
+
+using ddp::fail;
+using ddp::guarded;
+using ddp::hip_fail;
+
+namespace {
+
 // *captured: whether work enqueued on s is being recorded into a HIP graph
 // (stream capture) rather than run. The null stream cannot be captured.
 hipError_t is_captured(hipStream_t s, bool *captured) noexcept
@@ -74,21 +92,6 @@ hipError_t is_captured(hipStream_t s, bool *captured) noexcept
     const hipError_t e = hipStreamIsCapturing(s, &st);
     *captured = e == hipSuccess && st != hipStreamCaptureStatusNone;
     return e;
-}
-
-// Every entry point runs its body through this: the C ABI never lets an
-// exception out. Host memory exhaustion (std::bad_alloc from a container or
-// a message) becomes DDP_ERR_NOMEM; anything else DDP_ERR_INVALID.
-template <class F>
-int guarded(F &&body) noexcept
-{
-    try {
-        return body();
-    } catch (const std::bad_alloc &) {
-        return fail(DDP_ERR_NOMEM, kNoMemText);
-    } catch (...) {
-        return fail(DDP_ERR_INVALID, "internal error: unexpected exception in the host library");
-    }
 }
 
 std::string list_params(const std::vector<int32_t> &ps)
@@ -338,6 +341,7 @@ struct ddp_reducer {
     // valid while the area's generation is the one this reducer claimed
     int static_device = -1;
     uint64_t static_generation = 0;
+    std::vector<float *> flat;   // [W] the caller's flat buffers (empty without a device)
     hipStream_t compute = nullptr, comm = nullptr;
     // ev_ready: compute -> comm before a launch; ev_done: comm -> compute at
     // finish (device-scope release suffices between two streams of one
@@ -958,6 +962,7 @@ int create_reducer(const ddp_reducer_desc *desc, ddp_reducer **out, bool static_
         }
         e = hipMemcpy(workspace, host.data(), lay.total, hipMemcpyHostToDevice);
         if (e != hipSuccess) return hip_fail("workspace upload", e);
+        r->flat.assign(desc->flat, desc->flat + pv.W);
         uint8_t *ws = static_cast<uint8_t *>(workspace);
         r->tables.grads = copy_src ? reinterpret_cast<const void *const *>(ws + lay.grads_off) : nullptr;
         r->tables.flat = reinterpret_cast<float *const *>(ws + lay.flat_off);
@@ -1287,6 +1292,16 @@ int ddp_get_timings_impl(const ddp_reducer *r, int32_t *first_bucket, int32_t *n
 }
 
 }  // namespace
+
+namespace ddp {
+
+ReducerBuffers reducer_buffers(const ddp_reducer *r) noexcept
+{
+    return {r->pv.W, r->pv.reduce_scatter, r->pv.B, r->pv.bucket_bytes.data(), r->pv.bucket_flat.data(),
+            r->device ? r->flat.data() : nullptr};
+}
+
+}  // namespace ddp
 
 extern "C" {
 

@@ -1,4 +1,6 @@
-/* ddp.h — bucketed gradient reduction for data-parallel training, MI355X (gfx950).
+/* ddp.h — bucketed gradient reduction for data-parallel training, MI355X (gfx950):
+ * the reduction, the norm and clipping of its results, and the embedding's
+ * lookup and gradient.
  *
  * C ABI of libddp.so. Plain pointers and sizes only; every function returns
  * an int status (DDP_OK = 0, negative on error, text in ddp_last_error())
@@ -432,6 +434,178 @@ int ddp_get_launched(const ddp_reducer *r, int32_t *n_launched);
 int ddp_set_timing(ddp_reducer *r, int32_t enable);
 int ddp_get_timings(const ddp_reducer *r, int32_t *first_bucket, int32_t *n_buckets, float *ms, int32_t capacity,
                     int32_t *n);
+
+/* ---------------------------------------------------------------------------
+ * Gradient lists: the norm of all of a model's gradients, and clipping by it.
+ *
+ * What a training step does between the reduction and the optimizer: take the
+ * norm over every gradient of the model, and scale all of them by
+ * min(1, max_norm / (norm + 1e-6)). A list names the tensors once; the calls
+ * on it then cost one or two launches however many tensors it holds.
+ * ------------------------------------------------------------------------- */
+enum {
+    DDP_F32 = 0,
+    DDP_BF16 = 1,
+    DDP_F16 = 2
+};
+
+enum {
+    DDP_NORM_INF = 0,   /* max |g| */
+    DDP_NORM_L1 = 1,    /* sum |g| */
+    DDP_NORM_L2 = 2     /* sqrt(sum g^2) */
+};
+
+typedef struct ddp_grads ddp_grads;   /* opaque, owned by the library */
+
+typedef struct {
+    int32_t n_tensors;           /* N >= 0                                                          */
+    int32_t n_copies;            /* R >= 1 replicas that hold the same gradients: the norm is taken
+                                    over copy 0, clipping scales all of them                        */
+    const int64_t *numel;        /* [N] elements, >= 0                                              */
+    const int32_t *dtype;        /* [N] DDP_F32, DDP_BF16 or DDP_F16; NULL: all fp32                */
+    const void *const *grads;    /* [R*N] device pointers, entry r*N + i = copy r's tensor i, at any
+                                    multiple of the element's size, contiguous; of a tensor of no
+                                    elements the pointer is not looked at                           */
+    void *const *out;            /* [R*N] where clipping writes; NULL: in place                     */
+    const int32_t *out_dtype;    /* [N] types of `out`; NULL: as dtype. Only with `out`              */
+    void *workspace;             /* device memory of ddp_grads_workspace_bytes() bytes, 16-byte
+                                    aligned, for the list's tables                                  */
+    size_t workspace_bytes;
+} ddp_grads_desc;
+
+/* Device workspace a list needs for its tables (32 bytes a tensor and copy,
+ * 4 bytes per 8192 elements). Returns 0 and sets ddp_last_error() if the desc
+ * is invalid; pointers are not looked at. */
+size_t ddp_grads_workspace_bytes(const ddp_grads_desc *desc);
+
+/* Builds the list's tables and uploads them (synchronously) into the
+ * workspace, which must stay valid, as must the tensors, for as long as the
+ * list is used. The list is tied to the device that is current here. *out is
+ * set only on success.
+ * Errors: DDP_ERR_INVALID: bad sizes, types or alignment; a tensor that
+ * overlaps another (counted or scaled twice), or an `out` that overlaps any
+ * tensor or another `out`; DDP_ERR_HIP; DDP_ERR_NOMEM. */
+int ddp_grads_create(const ddp_grads_desc *desc, ddp_grads **out);
+
+/* The list of a reducer's results, clipped in place: the flat buffers that
+ * ddp_finish leaves. After an all-reduce the W flat buffers are W copies of
+ * one tensor. After a reduce-scatter the owners' chunks are the tensors (chunk
+ * c of every bucket in replica c's buffer), one copy of each; the rest of the
+ * buffers is neither read nor written. Gradients that no replica used keep
+ * what their slices held (ddp_set_local_used), and count with it. Queue the
+ * calls on the compute stream after ddp_finish. The list copies the pointers:
+ * it may outlive the reducer.
+ * Errors as ddp_grads_create; DDP_ERR_INVALID for a reducer without a device. */
+size_t ddp_reducer_grads_workspace_bytes(const ddp_reducer *r);
+int ddp_grads_from_reducer(const ddp_reducer *r, void *workspace, size_t workspace_bytes, ddp_grads **out);
+
+/* Releases the list's host state; touches no device memory. The workspace
+ * must outlive the calls still queued. NULL is a no-op. */
+int ddp_grads_destroy(ddp_grads *g);
+
+/* Device scratch that one call of ddp_grad_norm or ddp_clip_grad_norm needs
+ * (at most 16 KiB, at least 8 bytes). Its contents mean nothing between calls.
+ * A list is only read by the calls on it: any number of them may run at once,
+ * on any streams and from replayed graphs, as long as each has a scratch of
+ * its own (and no two scale the same tensors). */
+int ddp_grads_scratch_bytes(const ddp_grads *g, size_t *bytes);
+
+/* *norm (device, one float) = the norm of copy 0 of the list, on `stream`.
+ * Sums run in 64 bits in a fixed order and are rounded to fp32 once: the same
+ * list gives the same bits every time, and no square overflows. A NaN
+ * anywhere gives NaN, otherwise an infinity inf; a list of no elements 0.
+ * norm must not lie inside a tensor of the list. May be recorded into a HIP
+ * graph.
+ * Errors: DDP_ERR_INVALID (unknown norm, NULL or misaligned pointers, scratch
+ * missing or too small, another device current than the list's, a stream of
+ * another device), DDP_ERR_HIP. */
+int ddp_grad_norm(const ddp_grads *g, int32_t norm_type, float *norm, void *scratch, size_t scratch_bytes,
+                  void *stream);
+
+/* ddp_grad_norm, then every copy g of every tensor becomes
+ * R(g * f), f = min(1, max_norm / (norm + 1e-6)), in place or in `out`: f in
+ * fp32, the product in fp32, R one rounding to the output's type (fp16: inf
+ * beyond its range). With f = 1 an in-place list is left untouched. A NaN norm
+ * makes every result NaN, an infinite one makes finite gradients 0 and
+ * infinite ones NaN: look at *norm before the optimizer's step. The norm is
+ * written to *norm as it was before clipping.
+ * Errors as ddp_grad_norm; DDP_ERR_INVALID unless 0 <= max_norm < inf. */
+int ddp_clip_grad_norm(const ddp_grads *g, int32_t norm_type, float max_norm, float *norm, void *scratch,
+                       size_t scratch_bytes, void *stream);
+
+/* The scaling alone, with a norm that is given (device, one float): e.g. of
+ * several ranks' lists, summed. Errors as ddp_clip_grad_norm. */
+int ddp_clip_grads(const ddp_grads *g, float max_norm, const float *norm, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Embedding: the lookup of a table's rows, and the table's gradient.
+ *
+ * The embedding is the one parameter whose gradient is not a matrix product
+ * but a sum of rows by token. ddp_embedding_grad adds it straight to the
+ * parameter's place in the flat buffer (the fp32 main_grad of
+ * DDP_IN_BF16_ACCUM_F32 [MegatronDDP §1], a bucket view of DDP_IN_F32_VIEW
+ * [DDP-ch17 §17.5]) or writes a whole weight gradient for the reducer to read.
+ *
+ * The table may be one shard of a vocabulary: it holds the rows of the indices
+ * [first_row, first_row + n_rows). An index outside them, negative ones
+ * included, looks up a row of zeros and contributes no gradient; no index is
+ * ever an out-of-range access.
+ * ------------------------------------------------------------------------- */
+enum {
+    DDP_I32 = 0,
+    DDP_I64 = 1
+};
+
+typedef struct {
+    int64_t n_rows;         /* V, 0 <= V < 2^31 - 1                                                 */
+    int64_t width;          /* H, 0 <= H < 2^31                                                     */
+    int64_t first_row;      /* index of row 0                                                       */
+    int64_t padding_idx;    /* index whose positions contribute no gradient (it is looked up like
+                               any other); a negative value: none                                   */
+    int64_t table_stride;   /* elements from one row of the table to the next, >= H                 */
+    int64_t grad_stride;    /* the same of the gradient, >= H                                       */
+    int64_t act_stride;     /* elements between two positions' rows of the lookup's output (>= H) or
+                               of its gradient (>= 0: 0 is one row for every position)              */
+    float scale;            /* out = scale * row; the gradient is scaled by it too                  */
+    int32_t index_dtype;    /* DDP_I32 or DDP_I64                                                   */
+    int32_t table_dtype;    /* DDP_F32, DDP_BF16 or DDP_F16                                         */
+    int32_t grad_dtype;
+    int32_t act_dtype;
+} ddp_embedding_desc;
+
+/* out[t] = R(scale * table[tokens[t] - first_row]) for t in [0, n_tokens),
+ * n_tokens in [0, 2^30], 0
+ * for an index the table does not hold: the product in fp32, R one rounding to
+ * act_dtype. All pointers are device memory at multiples of their element's
+ * size; out must overlap neither table nor tokens. Elements of out between
+ * the rows are left alone. May be recorded into a HIP graph.
+ * Errors: DDP_ERR_INVALID (bad desc, NULL or misaligned pointers, a stream of
+ * another device than the current one), DDP_ERR_HIP. */
+int ddp_embedding_lookup(const ddp_embedding_desc *desc, const void *table, const void *tokens, int64_t n_tokens,
+                         void *out, void *stream);
+
+/* Device workspace of one ddp_embedding_grad call of up to n_tokens positions
+ * (8 bytes a position, 4 bytes a row, and the partial sums of frequent tokens:
+ * at most a quarter of n_tokens rows of fp32). Returns 0 and sets
+ * ddp_last_error() if the desc is invalid. */
+size_t ddp_embedding_grad_workspace_bytes(const ddp_embedding_desc *desc, int64_t n_tokens);
+
+/* grad[v] (+)= scale * sum of dout[t] over the positions t whose token is row
+ * v's, in position order: with accumulate != 0 the sum is added to what grad
+ * holds and rows without a position are not touched; with accumulate == 0
+ * grad's old contents are not read and rows without a position become 0. Sums
+ * are fp32, rounded once to grad_dtype. The order of the additions depends on
+ * the tokens alone: the same call gives the same bits every time (no
+ * floating-point atomics).
+ * The positions are sorted by token first (stable), then each row's are summed
+ * once. All pointers are device memory at multiples of their element's size
+ * (workspace: 256 bytes); grad must overlap no other argument. A workspace
+ * serves one call at a time: calls that may run at once, replays of captured
+ * ones included, need one each. May be recorded into a HIP graph.
+ * Errors: as ddp_embedding_lookup; DDP_ERR_INVALID for a missing or too small
+ * workspace. */
+int ddp_embedding_grad(const ddp_embedding_desc *desc, const void *dout, const void *tokens, int64_t n_tokens,
+                       void *grad, int32_t accumulate, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Text of the last error on this thread ("" if none). Never NULL. Where the
  * pages give PyTorch's wording of a Reducer error, the text starts with it
