@@ -66,7 +66,6 @@ EmbeddingArgs args_of(const ddp_embedding_desc &d, int64_t n_tokens)
     a.n_rows = d.n_rows;
     a.width = d.width;
     a.first_row = d.first_row;
-    a.padding_idx = d.padding_idx;
     a.table_stride = d.table_stride;
     a.grad_stride = d.grad_stride;
     a.act_stride = d.act_stride;
@@ -103,7 +102,7 @@ int64_t slabs_of(const ddp_embedding_desc &d)
     return std::max<int64_t>(1, ceil_div(d.width, 64 * (d.act_dtype == DDP_F32 ? 4 : 8)));
 }
 
-// Positions of a chunk: as many as still leave kWantedWaves waves, 8 to 64.
+// Positions of a chunk: as many as still leave kWantedWaves waves, 8 to 32.
 // Longer chunks cut fewer runs; the waves fill the chip.
 int32_t chunk_of(const ddp_embedding_desc &d, int64_t n_tokens)
 {
@@ -192,6 +191,10 @@ int grad(const ddp_embedding_desc *d, const void *dout, const void *tokens, int6
     // the rows are split over about 256 workgroups, one a CU, as far as the
     // counters of a range fit the LDS
     w.sort_rows = int32_t(std::min<int64_t>(ddp::kMaxSortRows, std::max<int64_t>(16, ceil_div(d->n_rows, 256))));
+    w.pad_row = -1;
+    if (d->padding_idx >= 0 && d->padding_idx >= d->first_row &&
+        uint64_t(d->padding_idx) - uint64_t(d->first_row) < uint64_t(d->n_rows))
+        w.pad_row = int32_t(d->padding_idx - d->first_row);
     const int64_t wide = ceil_div(d->width, 64);   // slabs of the narrowest kernel, an upper bound
     if ((w.n_chunks + (accumulate ? 0 : d->n_rows)) * wide > std::numeric_limits<int32_t>::max() - 8)
         return fail(DDP_ERR_INVALID, "n_tokens and n_rows times width are too large for one call");

@@ -12,12 +12,13 @@ constexpr int kSortThreads = 1024;             // 16 waves
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kMaxSortRows = 2048;             // rows of one sorting workgroup: 128 KiB of LDS counters
 
-// Sorted positions one wave sums (a chunk), at most.
-constexpr int kMaxChunk = 64;
+// Sorted positions one wave sums (a chunk), at most: it holds twice as many in
+// its 64 lanes.
+constexpr int kMaxChunk = 32;
 
 struct EmbeddingArgs {
     int64_t n_rows, width;
-    int64_t first_row, padding_idx;
+    int64_t first_row;
     int64_t table_stride, grad_stride, act_stride;
     int64_t n_tokens;
     float scale;
@@ -29,13 +30,14 @@ struct EmbeddingArgs {
 struct EmbeddingWork {
     int32_t *row;     // [T] rows of the sorted positions
     int32_t *pos;     // [T] the positions, sorted by row, then by position
-    int32_t *begin;   // [V + 1] where each row's positions begin; the last: how many there are
+    int32_t *begin;   // [V + 1] where each row's positions begin; the last: how many lie in the table
     float *first;     // [chunks][slots] sums of the pieces that begin a long run
     float *more;      // [chunks][slots] sums of the pieces that go on with one
     int64_t pitch;    // elements of one chunk's slot: the width rounded up
     int32_t chunk;    // positions of a chunk
     int32_t n_chunks;
     int32_t sort_rows;   // rows of one sorting workgroup
+    int32_t pad_row;     // the row whose positions count for nothing, or -1
 };
 
 hipError_t launch_lookup(const EmbeddingArgs &a, const void *table, const void *tokens, void *out, hipStream_t s);

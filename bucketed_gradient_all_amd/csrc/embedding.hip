@@ -116,14 +116,16 @@ __device__ __forceinline__ void store(void *base, int64_t e, const float (&v)[VE
     }
 }
 
-// The row of the token at t, or -1.
-__device__ __forceinline__ int row_of(const EmbeddingArgs &a, const void *tokens, int64_t t, bool drop_padding)
+// Data that no wave of the launch writes: uniform loads of it go through the
+// scalar cache.
+#define CONSTANT __attribute__((address_space(4)))
+
+// The row of a token, or -1.
+__device__ __forceinline__ int row_of(const EmbeddingArgs &a, int64_t tok)
 {
-    const int64_t tok = a.index64 ? ((const GLOBAL int64_t *)tokens)[t] : int64_t(((const GLOBAL int32_t *)tokens)[t]);
     // unsigned, so that no index wraps into the range
     const uint64_t r = uint64_t(tok) - uint64_t(a.first_row);
-    const bool pad = drop_padding && a.padding_idx >= 0 && tok == a.padding_idx;
-    return r < uint64_t(a.n_rows) && !pad ? int(r) : -1;
+    return r < uint64_t(a.n_rows) ? int(r) : -1;
 }
 
 constexpr int kWaves = 4;   // of a workgroup of the row kernels
@@ -148,7 +150,10 @@ lookup(EmbeddingArgs a, int slabs, const void *table, const void *tokens, void *
     int row[TOK];
     typename Raw<TABLE, VEC>::type x[TOK];
 #pragma unroll
-    for (int k = 0; k < TOK; ++k) row[k] = t0 + k < a.n_tokens ? row_of(a, tokens, t0 + k, false) : -1;
+    for (int k = 0; k < TOK; ++k) {
+        const int64_t t = min(t0 + k, a.n_tokens - 1);   // past the end: the last one again
+        row[k] = row_of(a, a.index64 ? ((const CONSTANT int64_t *)tokens)[t] : ((const CONSTANT int32_t *)tokens)[t]);
+    }
 #pragma unroll
     for (int k = 0; k < TOK; ++k)
         if (row[k] >= 0) x[k] = load<TABLE, VEC>(table, row[k] * a.table_stride + c.col);
@@ -164,16 +169,66 @@ lookup(EmbeddingArgs a, int slabs, const void *table, const void *tokens, void *
 }
 
 // ---------------------------------------------------------------- sort
-// Counters in LDS: counts[row in the range][wave], padded by a row's worth of
-// nothing; a wave's 64 lanes hit different rows' counters.
-__global__ void __launch_bounds__(kSortThreads) sort_tokens(EmbeddingArgs a, EmbeddingWork w, const void *tokens)
+// A workgroup's range of rows, as tests of a token: its row is below the range,
+// or in it (at `local`). Every workgroup puts every token to both tests, so
+// they are what the kernel spends its time on: two subtractions and two
+// comparisons a token, the rest on the scalar unit.
+struct Range {
+    uint64_t first, lo, hi;
+    __device__ __forceinline__ uint64_t row(int64_t tok) const { return uint64_t(tok) - first; }
+    __device__ __forceinline__ bool below(uint64_t r) const { return r < lo; }
+    __device__ __forceinline__ bool upto(uint64_t r) const { return r < hi; }
+};
+
+// Calls f(row, in range?, position) for the tokens [from, to) in order, 64 at
+// a time, and adds up those below the range. The loads of eight groups are in
+// flight together.
+template <class INDEX, class F>
+__device__ __forceinline__ uint32_t each_token(const Range &range, const INDEX *tokens, int from, int to, int lane, F f)
 {
-    extern __shared__ uint32_t counts[];   // [kSortWaves][rows]
+    constexpr int AHEAD = 8;
+    const GLOBAL INDEX *p = (const GLOBAL INDEX *)tokens;
+    uint32_t below = 0;
+    int i = from;
+    for (; i + 64 * AHEAD <= to; i += 64 * AHEAD) {
+        INDEX tok[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) tok[k] = p[i + k * 64 + lane];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const uint64_t r = range.row(tok[k]);
+            const bool low = range.below(r);
+            below += __popcll(__ballot(low));
+            f(r, range.upto(r) && !low, i + k * 64 + lane);
+        }
+    }
+    if (i < to) {   // the rest, with the last token in the place of those past it
+        INDEX tok[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) tok[k] = p[min(i + k * 64 + lane, to - 1)];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const bool there = i + k * 64 + lane < to;
+            const uint64_t r = range.row(tok[k]);
+            const bool low = range.below(r);
+            below += __popcll(__ballot(low && there));
+            f(r, range.upto(r) && !low && there, i + k * 64 + lane);
+        }
+    }
+    return below;
+}
+
+// Counters in LDS: counts[wave][row in the range].
+template <class INDEX>
+__global__ void __launch_bounds__(kSortThreads) sort_tokens(EmbeddingArgs a, EmbeddingWork w, const INDEX *tokens)
+{
+    extern __shared__ uint32_t counts[];
     __shared__ uint32_t sums[kSortWaves];
     __shared__ uint32_t below_sums[kSortWaves];
     const int tid = int(threadIdx.x), lane = tid % 64, wave = wave_of();
     const int lo = int(blockIdx.x) * w.sort_rows;
     const int rows = min(w.sort_rows, int(a.n_rows) - lo);   // the range [lo, lo + rows)
+    const Range range{uint64_t(a.first_row), uint64_t(lo), uint64_t(lo + rows)};
     for (int i = tid; i < rows * kSortWaves; i += kSortThreads) counts[i] = 0;
     __syncthreads();
 
@@ -182,20 +237,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_tokens(EmbeddingArgs a, Emb
     const int part = (T + kSortThreads - 1) / kSortThreads * 64;
     const int from = int(min(int64_t(T), int64_t(part) * wave)), to = int(min(int64_t(T), int64_t(from) + part));
     uint32_t *mine = counts + wave * rows;
-    uint32_t below = 0;
-    constexpr int AHEAD = 8;
-    for (int64_t i = from; i < to; i += 64 * AHEAD) {
-        int r[AHEAD];
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) r[k] = i + k * 64 + lane < to ? row_of(a, tokens, i + k * 64 + lane, true) : -1;
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            below += r[k] >= 0 && r[k] < lo;
-            if (r[k] >= lo && r[k] < lo + rows) atomicAdd(&mine[r[k] - lo], 1u);
-        }
-    }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) below += __shfl_xor(below, d);
+    const uint32_t below = each_token(range, tokens, from, to, lane, [&](uint64_t r, bool in, int) {
+        if (in) atomicAdd(&mine[int(r) - lo], 1u);
+    });
     if (lane == 0) below_sums[wave] = below;
     __syncthreads();
 
@@ -244,123 +288,78 @@ __global__ void __launch_bounds__(kSortThreads) sort_tokens(EmbeddingArgs a, Emb
     // put the positions in place, each wave its own part in order: the lanes
     // of one row find each other by the bits of its number
     const int bits = 32 - __clz(max(rows - 1, 1));
-    for (int64_t i = from; i < to; i += 64 * AHEAD) {
-        int r[AHEAD];
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) r[k] = i + k * 64 + lane < to ? row_of(a, tokens, i + k * 64 + lane, true) : -1;
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            const bool in = r[k] >= lo && r[k] < lo + rows;
-            uint64_t same = __ballot(in);
-            if (same == 0) continue;
-            const int local = r[k] - lo;
-            for (int b = 0; b < bits; ++b) {
-                const uint64_t set = __ballot(in && ((local >> b) & 1));
-                same &= (local >> b) & 1 ? set : ~set;
-            }
-            if (in) {
-                const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
-                const int leader = __ffsll((unsigned long long)same) - 1;
-                uint32_t place = 0;
-                if (lane == leader) place = atomicAdd(&mine[local], uint32_t(__popcll(same)));
-                place = __shfl(place, leader) + rank;
-                w.row[place] = r[k];
-                w.pos[place] = int(i + k * 64 + lane);
-            }
+    each_token(range, tokens, from, to, lane, [&](uint64_t r, bool in, int pos) {
+        uint64_t same = __ballot(in);
+        if (same == 0) return;
+        const int local = int(r) - lo;
+        for (int b = 0; b < bits; ++b) {
+            const bool bit = (local >> b) & 1;
+            const uint64_t set = __ballot(in && bit);
+            same &= bit ? set : ~set;
         }
-    }
+        if (in) {
+            const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
+            const int leader = __ffsll((unsigned long long)same) - 1;
+            uint32_t place = 0;
+            if (lane == leader) place = atomicAdd(&mine[local], uint32_t(__popcll(same)));
+            place = __shfl(place, leader) + rank;
+            w.row[place] = int(r);
+            w.pos[place] = pos;
+        }
+    });
 }
 
 // ---------------------------------------------------------------- sum
-template <int GRAD, int VEC>
-__device__ __forceinline__ void put(const EmbeddingArgs &a, void *grad, bool accumulate, int row, const Columns<VEC> &c,
+template <int GRAD, int VEC, bool ACC>
+__device__ __forceinline__ void put(const EmbeddingArgs &a, void *grad, int row, const Columns<VEC> &c,
                                     const typename Raw<GRAD, VEC>::type &old, const float (&sum)[VEC])
 {
     if (!c.on) return;
     float v[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j)
-        v[j] = accumulate ? __fmaf_rn(a.scale, sum[j], widen<GRAD>(old[j])) : __fmul_rn(a.scale, sum[j]);
+        v[j] = ACC ? __fmaf_rn(a.scale, sum[j], widen<GRAD>(old[j])) : __fmul_rn(a.scale, sum[j]);
     store<GRAD, VEC>(grad, row * a.grad_stride + c.col, v, c.skip);
 }
 
-template <int ACT, int GRAD, int VEC>
-struct Summer {
-    static constexpr int AHEAD = 8;   // rows of dout (and of grad, where a run ends) in flight
-    const EmbeddingArgs &a;
-    const EmbeddingWork &w;
-    const Columns<VEC> &c;
-    const void *dout;
-    void *grad;
-    bool accumulate;
-
-    // the positions [i, end) of whole runs
-    __device__ __forceinline__ void runs(int i, const int end) const
-    {
-        float sum[VEC] = {};
-        while (i < end) {
-            int row[AHEAD + 1];
-            typename Raw<ACT, VEC>::type x[AHEAD];
-            typename Raw<GRAD, VEC>::type old[AHEAD];
-            bool last[AHEAD];
-            const int n = min(AHEAD, end - i);
-#pragma unroll
-            for (int k = 0; k <= AHEAD; ++k) row[k] = w.row[min(i + k, end - 1)];
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {
-                last[k] = k < n && (i + k == end - 1 || row[k + 1] != row[k]);
-                if (k < n) x[k] = load<ACT, VEC>(dout, w.pos[i + k] * a.act_stride + c.col);
-                if (last[k] && accumulate) old[k] = load<GRAD, VEC>(grad, row[k] * a.grad_stride + c.col);
-            }
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {
-                if (k >= n) break;
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) sum[j] = __fadd_rn(sum[j], widen<ACT>(x[k][j]));
-                if (last[k]) {
-                    put<GRAD, VEC>(a, grad, accumulate, row[k], c, old[k], sum);
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) sum[j] = 0.0f;
-                }
-            }
-            i += n;
-        }
-    }
-
-    // one piece of a long run
-    __device__ __forceinline__ void piece(int i, const int end, float *slot) const
-    {
-        float sum[VEC] = {};
-        while (i < end) {
-            typename Raw<ACT, VEC>::type x[AHEAD];
-            const int n = min(AHEAD, end - i);
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k)
-                if (k < n) x[k] = load<ACT, VEC>(dout, w.pos[i + k] * a.act_stride + c.col);
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {
-                if (k >= n) break;
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) sum[j] = __fadd_rn(sum[j], widen<ACT>(x[k][j]));
-            }
-            i += n;
-        }
-        if (c.on) store<DDP_F32, VEC>(slot, c.col, sum, c.skip);
-    }
-};
-
-template <int ACT, int GRAD, int VEC>
-__global__ void __launch_bounds__(kWaves * 64)
-sum_runs(EmbeddingArgs a, EmbeddingWork w, int slabs, int tasks, int accumulate, const void *dout, void *grad)
+// A use of a loaded value that changes nothing: the compiler waits for the
+// load here.
+template <class T>
+__device__ __forceinline__ void arrive(T &v)
 {
+    if constexpr (sizeof(T) >= 4) {
+#pragma unroll
+        for (int i = 0; i < int(sizeof(T) / 4); ++i) {
+            uint32_t word;
+            __builtin_memcpy(&word, reinterpret_cast<const char *>(&v) + 4 * i, 4);
+            asm volatile("" : "+v"(word));
+            __builtin_memcpy(reinterpret_cast<char *>(&v) + 4 * i, &word, 4);
+        }
+    } else {
+        uint32_t word = v[0];
+        asm volatile("" : "+v"(word));
+        v[0] = static_cast<unsigned short>(word);
+    }
+}
+
+// A wave keeps the rows and positions of its chunk and of as many entries
+// after it in its lanes (a chunk is at most 32 long), so that the addresses of
+// a batch are known without a load and all of a batch's loads, of dout and of
+// the gradient's rows where a run ends, are in flight together.
+template <int ACT, int GRAD, int VEC, bool ACC>
+__global__ void __launch_bounds__(kWaves * 64)
+sum_runs(EmbeddingArgs a, EmbeddingWork w, int slabs, int tasks, const void *dout, void *grad)
+{
+    constexpr int AHEAD = 8;
     const int task = int(blockIdx.x) * kWaves + wave_of();
     const int lane = int(threadIdx.x) % 64;
+    const CONSTANT int32_t *begin = (const CONSTANT int32_t *)w.begin;
     if (task >= tasks) {
         // beyond the chunks: rows without a position, when the whole gradient
         // is written
         const int64_t z = int64_t(task) - (tasks + kWaves - 1) / kWaves * kWaves;
         const int64_t row = z / slabs;
-        if (accumulate || z < 0 || row >= a.n_rows || w.begin[row] != w.begin[row + 1]) return;
+        if (ACC || z < 0 || row >= a.n_rows || (begin[row] != begin[row + 1] && row != w.pad_row)) return;
         const Columns<VEC> c(z - row * slabs, lane, a.width);
         const float none[VEC] = {};
         if (c.on) store<GRAD, VEC>(grad, row * a.grad_stride + c.col, none, c.skip);
@@ -368,82 +367,178 @@ sum_runs(EmbeddingArgs a, EmbeddingWork w, int slabs, int tasks, int accumulate,
     }
     const int chunk = task / slabs;
     const Columns<VEC> c(task - chunk * slabs, lane, a.width);
-    const int valid = w.begin[a.n_rows];
+    const int valid = begin[a.n_rows];
     const int i0 = chunk * w.chunk;
     if (i0 >= valid) return;
-    const int border = min(i0 + w.chunk, valid);
-    const Summer<ACT, GRAD, VEC> s{a, w, c, dout, grad, accumulate != 0};
+    const int at = min(i0 + lane, valid - 1);
+    const int my_row = ((const GLOBAL int32_t *)w.row)[at];
+    const int my_pos = ((const GLOBAL int32_t *)w.pos)[at];
+    const int my_begin = ((const GLOBAL int32_t *)w.begin)[my_row];
+    const int my_end = ((const GLOBAL int32_t *)w.begin)[my_row + 1];
 
-    int i = i0, end = border;
-    const int head = w.row[i0], head_begin = w.begin[head], head_end = w.begin[head + 1];
+    // entries [begin_at, end) of the lanes, the runs' last ones, and those whose sum
+    // goes to a slot
+    const int border = min(w.chunk, valid - i0);
+    uint64_t last = __ballot(i0 + lane == my_end - 1);
+    uint64_t to_more = 0, to_first = 0;
+    int begin_at = 0, end = border;
+    const int head_begin = __builtin_amdgcn_readlane(my_begin, 0), head_end = __builtin_amdgcn_readlane(my_end, 0);
     if (head_begin < i0) {   // goes on from an earlier chunk: ours if it is long, that chunk's if not
-        i = min(head_end, border);
-        if (head_end - head_begin > w.chunk) s.piece(i0, i, w.more + int64_t(chunk) * w.pitch);
+        const int stop = min(head_end - i0, border);
+        if (head_end - head_begin > w.chunk)
+            to_more = uint64_t(1) << (stop - 1);
+        else
+            begin_at = stop;
     }
-    if (i >= border) return;
-    const int tail = w.row[border - 1], tail_begin = w.begin[tail], tail_end = w.begin[tail + 1];
-    if (tail_end > border) {   // goes on into the next chunk
-        if (tail_end - tail_begin > w.chunk) {
-            s.piece(tail_begin, border, w.first + int64_t(chunk) * w.pitch);
-            end = tail_begin;
-        } else {
-            end = tail_end;
+    const int tail_begin = __builtin_amdgcn_readlane(my_begin, border - 1);
+    const int tail_end = __builtin_amdgcn_readlane(my_end, border - 1);
+    if (tail_begin >= i0 && tail_end > i0 + border) {   // begins here, goes on into the next chunk
+        if (tail_end - tail_begin > w.chunk)
+            to_first = uint64_t(1) << (border - 1);
+        else
+            end = tail_end - i0;
+    }
+    last |= to_more | to_first;
+
+    // the padding row's positions are sorted like any other's and left out
+    // here: at most one stretch [skip, resume) of the entries
+    const uint64_t pads = __ballot(my_row == w.pad_row && i0 + lane < valid);
+    const int skip = pads ? __ffsll((unsigned long long)pads) - 1 : 64, resume = pads ? 64 - __clzll(pads) : 64;
+
+    float sum[VEC] = {};
+    const uint64_t rows = last & ~(to_more | to_first);
+    for (int part = 0; part < 2; ++part) {
+        const int stop = part ? end : min(end, skip);
+        for (int e = part ? max(begin_at, resume) : begin_at; e < stop; e += AHEAD) {
+            typename Raw<ACT, VEC>::type x[AHEAD];
+            typename Raw<GRAD, VEC>::type old[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const int64_t pos = __builtin_amdgcn_readlane(my_pos, min(e + k, stop - 1));
+                x[k] = load<ACT, VEC>(dout, pos * a.act_stride + c.col);
+            }
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                if (ACC && e + k < stop && (rows >> (e + k)) & 1) {
+                    const int64_t row = __builtin_amdgcn_readlane(my_row, e + k);
+                    old[k] = load<GRAD, VEC>(grad, row * a.grad_stride + c.col);
+                }
+            }
+            // All of the batch's loads are waited for here, once. Left to
+            // itself the compiler waits where each value is used, which is
+            // after the stores of the runs before it, and a wait for a load
+            // there waits for those stores too.
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                arrive(x[k]);
+                if (ACC) arrive(old[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                if (e + k < stop) {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) sum[j] = __fadd_rn(sum[j], widen<ACT>(x[k][j]));
+                    const uint64_t here = uint64_t(1) << (e + k);
+                    if (last & here) {
+                        if ((to_more | to_first) & here) {
+                            float *slot = (to_more & here ? w.more : w.first) + int64_t(chunk) * w.pitch;
+                            if (c.on) store<DDP_F32, VEC>(slot, c.col, sum, c.skip);
+                        } else {
+                            put<GRAD, VEC, ACC>(a, grad, __builtin_amdgcn_readlane(my_row, e + k), c, old[k], sum);
+                        }
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j) sum[j] = 0.0f;
+                    }
+                }
+            }
         }
     }
-    s.runs(i, end);
 }
 
 // ---------------------------------------------------------------- join
-constexpr int kJoinWaves = 16;
+// A workgroup looks after the long runs that begin in kJoinChunks chunks, over
+// a slab of columns. Runs of few pieces go one to a wave; the pieces of one of
+// many are split over the four waves and the waves' sums added in order.
+constexpr int kJoinChunks = 8;
+constexpr int kFewPieces = 16;
 
-// The workgroup of the chunk in which a long run begins adds up the run's
-// pieces: each wave a contiguous part of them, then the waves in order.
-template <int GRAD, int VEC>
-__global__ void __launch_bounds__(kJoinWaves * 64)
-join_runs(EmbeddingArgs a, EmbeddingWork w, int slabs, int accumulate, void *grad)
+// Pieces [k, to) of a long run.
+template <int VEC>
+__device__ __forceinline__ void add_pieces(const EmbeddingWork &w, const Columns<VEC> &c, int k, int to,
+                                           float (&sum)[VEC])
 {
-    __shared__ float part[kJoinWaves][64 * VEC];
-    const int chunk = int(blockIdx.x) / slabs, slab = int(blockIdx.x) - chunk * slabs;
-    const int valid = w.begin[a.n_rows];
-    const int i0 = chunk * w.chunk, border = i0 + w.chunk;
-    if (border >= valid) return;
-    const int row = w.row[border - 1], run_begin = w.begin[row], run_end = w.begin[row + 1];
-    if (run_begin < i0 || run_end <= border || run_end - run_begin <= w.chunk) return;
-    const int wave = wave_of(), lane = int(threadIdx.x) % 64;
-    const Columns<VEC> c(slab, lane, a.width);
-    const int pieces = (run_end - 1) / w.chunk - chunk;   // after the first
-    const int each = (pieces + kJoinWaves - 1) / kJoinWaves;
-    int k = chunk + 1 + wave * each;
-    const int to = min(chunk + 1 + pieces, k + each);
-    float sum[VEC] = {};
     constexpr int AHEAD = 8;
-    while (k < to) {
+    for (; k < to; k += AHEAD) {
         typename Raw<DDP_F32, VEC>::type x[AHEAD];
-        const int n = min(AHEAD, to - k);
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) x[j] = load<DDP_F32, VEC>(w.more + int64_t(min(k + j, to - 1)) * w.pitch, c.col);
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j)
-            if (j < n) x[j] = load<DDP_F32, VEC>(w.more + int64_t(k + j) * w.pitch, c.col);
+            if (k + j < to) {
 #pragma unroll
-        for (int j = 0; j < AHEAD; ++j) {
-            if (j >= n) break;
+                for (int e = 0; e < VEC; ++e) sum[e] = __fadd_rn(sum[e], x[j][e]);
+            }
+    }
+}
+
+template <int GRAD, int VEC, bool ACC>
+__global__ void __launch_bounds__(kWaves * 64) join_runs(EmbeddingArgs a, EmbeddingWork w, int slabs, void *grad)
+{
+    __shared__ float part[kWaves][VEC][64];
+    const int group = int(blockIdx.x) / slabs, slab = int(blockIdx.x) - group * slabs;
+    const int wave = wave_of(), lane = int(threadIdx.x) % 64;
+    const CONSTANT int32_t *begin = (const CONSTANT int32_t *)w.begin;
+    const int valid = begin[a.n_rows];
+    // lane k looks at chunk k of the group
+    const int chunk = group * kJoinChunks + lane, i0 = chunk * w.chunk, border = i0 + w.chunk;
+    int row = 0, pieces = 0;
+    if (lane < kJoinChunks && chunk < w.n_chunks && border < valid) {
+        row = ((const GLOBAL int32_t *)w.row)[border - 1];
+        const int b = ((const GLOBAL int32_t *)w.begin)[row], e = ((const GLOBAL int32_t *)w.begin)[row + 1];
+        if (row != w.pad_row && b >= i0 && e > border && e - b > w.chunk) pieces = (e - 1) / w.chunk - chunk;   // after the first
+    }
+    uint64_t few = __ballot(pieces > 0 && pieces <= kFewPieces), many = __ballot(pieces > kFewPieces);
+    if ((few | many) == 0) return;
+    const Columns<VEC> c(slab, lane, a.width);
+
+    for (; many; many &= many - 1) {
+        const int k = __ffsll((unsigned long long)many) - 1;
+        const int n = __builtin_amdgcn_readlane(pieces, k), first = group * kJoinChunks + k;
+        const int64_t r = __builtin_amdgcn_readlane(row, k);
+        const int each = (n + kWaves - 1) / kWaves;
+        float sum[VEC] = {};
+        add_pieces<VEC>(w, c, first + 1 + wave * each, min(first + 1 + n, first + 1 + (wave + 1) * each), sum);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) sum[e] = __fadd_rn(sum[e], x[j][e]);
+        for (int e = 0; e < VEC; ++e) part[wave][e][lane] = sum[e];
+        __syncthreads();
+        if (wave == 0) {
+            typename Raw<GRAD, VEC>::type old;
+            if (ACC) old = load<GRAD, VEC>(grad, r * a.grad_stride + c.col);
+            const typename Raw<DDP_F32, VEC>::type x = load<DDP_F32, VEC>(w.first + int64_t(first) * w.pitch, c.col);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                sum[e] = x[e];
+#pragma unroll
+                for (int v = 0; v < kWaves; ++v) sum[e] = __fadd_rn(sum[e], part[v][e][lane]);
+            }
+            put<GRAD, VEC, ACC>(a, grad, int(r), c, old, sum);
         }
-        k += n;
+        __syncthreads();
     }
+    for (int turn = 0; few; few &= few - 1, ++turn) {
+        if (turn % kWaves != wave) continue;
+        const int k = __ffsll((unsigned long long)few) - 1;
+        const int n = __builtin_amdgcn_readlane(pieces, k), first = group * kJoinChunks + k;
+        const int64_t r = __builtin_amdgcn_readlane(row, k);
+        typename Raw<GRAD, VEC>::type old;
+        if (ACC) old = load<GRAD, VEC>(grad, r * a.grad_stride + c.col);
+        const typename Raw<DDP_F32, VEC>::type x = load<DDP_F32, VEC>(w.first + int64_t(first) * w.pitch, c.col);
+        float sum[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) part[wave][e * 64 + lane] = sum[e];
-    __syncthreads();
-    if (wave != 0) return;
-    typename Raw<GRAD, VEC>::type old;
-    if (accumulate) old = load<GRAD, VEC>(grad, row * a.grad_stride + c.col);
-    const typename Raw<DDP_F32, VEC>::type x = load<DDP_F32, VEC>(w.first + int64_t(chunk) * w.pitch, c.col);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        sum[e] = x[e];
-        for (int v = 0; v < kJoinWaves; ++v) sum[e] = __fadd_rn(sum[e], part[v][e * 64 + lane]);
+        for (int e = 0; e < VEC; ++e) sum[e] = x[e];
+        add_pieces<VEC>(w, c, first + 1, first + 1 + n, sum);
+        put<GRAD, VEC, ACC>(a, grad, int(r), c, old, sum);
     }
-    put<GRAD, VEC>(a, grad, accumulate != 0, row, c, old, sum);
 }
 
 template <int VEC>
@@ -459,7 +554,7 @@ hipError_t lookup_vec(const EmbeddingArgs &a, const void *table, const void *tok
     // four rows a wave once that leaves every CU sixteen waves
     const bool four = a.n_tokens * slabs >= 4 * 256 * 16;
     const int64_t tasks = (four ? (a.n_tokens + 3) / 4 : a.n_tokens) * slabs;
-    const dim3 g(unsigned((tasks + kWaves - 1) / kWaves)), b(kWaves * 64);
+    const dim3 g(static_cast<unsigned>((tasks + kWaves - 1) / kWaves)), b(kWaves * 64);
     if (four)
         hipLaunchKernelGGL((lookup<TABLE, ACT, VEC, 4>), g, b, 0, s, a, int(slabs), table, tokens, out);
     else
@@ -494,8 +589,11 @@ hipError_t sum_vec(const EmbeddingArgs &a, const void *dout, void *grad, bool ac
     const int64_t fill = accumulate ? 0 : a.n_rows * slabs;
     const int64_t blocks = (tasks + kWaves - 1) / kWaves + (fill + kWaves - 1) / kWaves;
     if (blocks == 0) return hipSuccess;
-    hipLaunchKernelGGL((sum_runs<ACT, GRAD, VEC>), dim3(unsigned(blocks)), dim3(kWaves * 64), 0, s, a, w, int(slabs),
-                       int(tasks), accumulate ? 1 : 0, dout, grad);
+    const dim3 g(static_cast<unsigned>(blocks)), b(kWaves * 64);
+    if (accumulate)
+        hipLaunchKernelGGL((sum_runs<ACT, GRAD, VEC, true>), g, b, 0, s, a, w, int(slabs), int(tasks), dout, grad);
+    else
+        hipLaunchKernelGGL((sum_runs<ACT, GRAD, VEC, false>), g, b, 0, s, a, w, int(slabs), int(tasks), dout, grad);
     return hipGetLastError();
 }
 
@@ -519,19 +617,22 @@ hipError_t sum_grad(const EmbeddingArgs &a, const void *dout, void *grad, bool a
     }
 }
 
+template <int GRAD, int VEC>
+hipError_t join_vec(const EmbeddingArgs &a, void *grad, bool accumulate, const EmbeddingWork &w, hipStream_t s)
+{
+    const int64_t slabs = slabs_of<VEC>(a.width);
+    const dim3 g(static_cast<unsigned>((w.n_chunks + kJoinChunks - 1) / kJoinChunks * slabs)), b(kWaves * 64);
+    if (accumulate)
+        hipLaunchKernelGGL((join_runs<GRAD, VEC, true>), g, b, 0, s, a, w, int(slabs), grad);
+    else
+        hipLaunchKernelGGL((join_runs<GRAD, VEC, false>), g, b, 0, s, a, w, int(slabs), grad);
+    return hipGetLastError();
+}
+
 template <int GRAD>
 hipError_t join_grad(const EmbeddingArgs &a, void *grad, bool accumulate, const EmbeddingWork &w, hipStream_t s)
 {
-    const dim3 b(kJoinWaves * 64);
-    if (a.width >= 4) {
-        const int slabs = slabs_of<4>(a.width);
-        hipLaunchKernelGGL((join_runs<GRAD, 4>), dim3(unsigned(int64_t(w.n_chunks) * slabs)), b, 0, s, a, w, slabs,
-                           accumulate ? 1 : 0, grad);
-    } else {
-        hipLaunchKernelGGL((join_runs<GRAD, 1>), dim3(unsigned(w.n_chunks)), b, 0, s, a, w, 1, accumulate ? 1 : 0,
-                           grad);
-    }
-    return hipGetLastError();
+    return a.width >= 4 ? join_vec<GRAD, 4>(a, grad, accumulate, w, s) : join_vec<GRAD, 1>(a, grad, accumulate, w, s);
 }
 
 }  // namespace
@@ -549,7 +650,11 @@ hipError_t launch_sort(const EmbeddingArgs &a, const void *tokens, const Embeddi
 {
     const int groups = int((a.n_rows + w.sort_rows - 1) / w.sort_rows);
     const unsigned lds = unsigned(w.sort_rows) * kSortWaves * sizeof(uint32_t);
-    hipLaunchKernelGGL(sort_tokens, dim3(unsigned(groups)), dim3(kSortThreads), lds, s, a, w, tokens);
+    const dim3 g(static_cast<unsigned>(groups)), b(kSortThreads);
+    if (a.index64)
+        hipLaunchKernelGGL((sort_tokens<int64_t>), g, b, lds, s, a, w, static_cast<const int64_t *>(tokens));
+    else
+        hipLaunchKernelGGL((sort_tokens<int32_t>), g, b, lds, s, a, w, static_cast<const int32_t *>(tokens));
     return hipGetLastError();
 }
 

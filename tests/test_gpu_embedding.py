@@ -432,3 +432,17 @@ def test_two_gradients_at_once_on_two_streams():
     torch.cuda.synchronize()
     for c, b in zip(cases, before):
         c.check_grad(b, True)
+
+
+@pytest.mark.parametrize("lead", range(20))
+def test_padding_between_other_rows_of_a_chunk(lead):
+    """The padding row's positions lie between other rows' in the sorted order,
+    at every offset from the chunks' borders."""
+    torch = _torch()
+    tok = torch.cat([torch.arange(lead), torch.full((5 + lead,), 30), torch.arange(31, 60), torch.full((40,), 61)])
+    tok = tok[torch.randperm(tok.numel(), generator=torch.Generator().manual_seed(lead))]
+    for accumulate in (True, False):
+        c = Case(tok.numel(), 64, 24, padding=30, seed=lead)
+        c.host_tokens = tok
+        c.tokens.copy_(tok)
+        c.run_grad(accumulate)
