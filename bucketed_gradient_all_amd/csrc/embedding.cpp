@@ -97,13 +97,24 @@ int check_device(hipStream_t s)
 // Waves that share the positions of the sum, at most, before chunks grow.
 constexpr int64_t kWantedWaves = 8192;
 
+// Positions from which a range of rows is sorted by two, and by four
+// workgroups. 8191 positions of 32000 rows: 9.2 us with one, 9.4 with two, 12.1
+// with four; 32768: 21.6, 16.6, 15.0 (eight: 21.2).
+constexpr int64_t kSomeTokens = 16384, kManyTokens = 32768;
+
+// Bytes of dout from which it is read past the caches: well below the 256 MiB
+// of the last cache it may still lie there from the kernel that wrote it.
+constexpr int64_t kStreamBytes = int64_t(64) << 20;
+
 int64_t slabs_of(const ddp_embedding_desc &d)
 {
-    return std::max<int64_t>(1, ceil_div(d.width, 64 * (d.act_dtype == DDP_F32 ? 4 : 8)));
+    return std::max<int64_t>(1, ceil_div(d.width, 64 * ddp::sum_vector(d.act_dtype, d.grad_dtype)));
 }
 
 // Positions of a chunk: as many as still leave kWantedWaves waves, 8 to 32.
-// Longer chunks cut fewer runs; the waves fill the chip.
+// Longer chunks cut fewer runs and leave the join less; the waves fill the chip
+// (32768 positions of 2048 columns: chunks of 32 56.2 us and the join 5.5, of
+// 16 53.8 and 7.6, of 8 56.0 and 12.6).
 int32_t chunk_of(const ddp_embedding_desc &d, int64_t n_tokens)
 {
     int32_t c = 8;
@@ -188,9 +199,12 @@ int grad(const ddp_embedding_desc *d, const void *dout, const void *tokens, int6
     w.pitch = l.pitch;
     w.chunk = chunk_of(*d, n);
     w.n_chunks = int32_t(ceil_div(n, w.chunk));
-    // the rows are split over about 256 workgroups, one a CU, as far as the
-    // counters of a range fit the LDS
-    w.sort_rows = int32_t(std::min<int64_t>(ddp::kMaxSortRows, std::max<int64_t>(16, ceil_div(d->n_rows, 256))));
+    // about 256 workgroups, one a CU: ranges of rows, as far as a range's
+    // counters fit the LDS, times the workgroups of a range
+    w.splits = n >= kManyTokens ? 4 : n >= kSomeTokens ? 2 : 1;
+    w.sort_rows = int32_t(
+        std::min<int64_t>(ddp::kMaxSortRows, std::max<int64_t>(16, ceil_div(d->n_rows, 256 / w.splits))));
+    w.stream = n * d->width * element_size(d->act_dtype) > kStreamBytes;
     w.pad_row = -1;
     if (d->padding_idx >= 0 && d->padding_idx >= d->first_row &&
         uint64_t(d->padding_idx) - uint64_t(d->first_row) < uint64_t(d->n_rows))

@@ -10,11 +10,17 @@ namespace ddp {
 
 constexpr int kSortThreads = 1024;             // 16 waves
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kMaxSortRows = 2048;             // rows of one sorting workgroup: 128 KiB of LDS counters
+constexpr int kMaxSortRows = 2048;             // rows of one sorting workgroup: 144 KiB of LDS counters
 
 // Sorted positions one wave sums (a chunk), at most: it holds twice as many in
 // its 64 lanes.
 constexpr int kMaxChunk = 32;
+
+// Columns a lane sums: 16 bytes of the wider type.
+constexpr int sum_vector(int act_dtype, int grad_dtype)
+{
+    return act_dtype == 0 || grad_dtype == 0 ? 4 : 8;   // 0: DDP_F32
+}
 
 struct EmbeddingArgs {
     int64_t n_rows, width;
@@ -37,6 +43,8 @@ struct EmbeddingWork {
     int32_t chunk;    // positions of a chunk
     int32_t n_chunks;
     int32_t sort_rows;   // rows of one sorting workgroup
+    int32_t splits;      // sorting workgroups of one range of rows
+    int32_t stream;      // read dout past the caches
     int32_t pad_row;     // the row whose positions count for nothing, or -1
 };
 
