@@ -22,7 +22,8 @@ struct ddp_grads {
     int device = -1;
     int blocks = 1;        // workgroups of the norm's pass
     int clip_blocks = 1;   // workgroups of the clipping pass
-    bool small = false;    // one workgroup does it all
+    bool small = false;    // one workgroup clips it
+    bool parts = false;    // clipping runs a workgroup a part of a tile, the norm finished before
 };
 
 namespace {
@@ -167,12 +168,18 @@ int create(const ddp_grads_desc *d, ddp_grads **out)
     g->tables.tile_seg = reinterpret_cast<const int32_t *>(ws + segs_bytes);
     g->tables.norm_tiles = norm_tiles;
     g->tables.all_tiles = int32_t(tile_seg.size());
-    g->small = g->tables.all_tiles <= ddp::kSmallTiles;
-    // eight workgroups a CU keep every wave slot that the registers allow
-    // filled, and leave at most kMaxPartials partials to sum
-    const int most = std::min(ddp::kMaxPartials, std::max(1, 8 * cus));
-    g->blocks = std::max(1, std::min(norm_tiles, most));
-    g->clip_blocks = std::max(1, std::min(g->tables.all_tiles, most));
+    g->tables.in_place = d->out == nullptr;
+    g->small = g->tables.all_tiles <= ddp::kSmallClip;
+    // workgroups that go from tile to tile, as many as fill the chip. The norm
+    // does best with four a CU (953M bf16 elements 285 us, eight 294, two 292)
+    // and leaves as many partials; clipping has stores too and takes eight.
+    g->blocks = std::max(1, std::min({norm_tiles, ddp::kMaxPartials, 4 * cus}));
+    g->clip_blocks = std::max(1, std::min(g->tables.all_tiles, 8 * cus));
+    // Into other buffers every tensor is written, so a workgroup a part of a
+    // tile pays. In place there is mostly nothing to do but to see that the
+    // norm is below the bound, which 2048 workgroups do in 7 us; 41116, one a
+    // tile, took 11.
+    g->parts = !g->tables.in_place && g->tables.all_tiles > ddp::kManyTiles;
     *out = g.release();
     return DDP_OK;
 }
@@ -334,7 +341,7 @@ int ddp_grad_norm(const ddp_grads *g, int32_t norm_type, float *norm, void *scra
         const int rc = check_call(g, norm_type, norm, scratch, scratch_bytes, s);
         if (rc != DDP_OK) return rc;
         hipError_t e;
-        if (g->tables.norm_tiles <= ddp::kSmallTiles) {
+        if (g->tables.norm_tiles <= ddp::kSmallNorm) {
             e = ddp::launch_small(norm_type, g->tables, false, 0.0f, norm, s);
         } else {
             e = ddp::launch_norm_partials(norm_type, g->tables, g->blocks, scratch, s);
@@ -357,9 +364,13 @@ int ddp_clip_grad_norm(const ddp_grads *g, int32_t norm_type, float max_norm, fl
             e = ddp::launch_small(norm_type, g->tables, true, max_norm, norm, s);
         } else {
             e = ddp::launch_norm_partials(norm_type, g->tables, g->blocks, scratch, s);
-            if (e == hipSuccess)
+            if (e == hipSuccess && g->parts) {
+                e = ddp::launch_norm_finish(norm_type, g->blocks, scratch, norm, s);
+                if (e == hipSuccess) e = ddp::launch_clip_parts(g->tables, {max_norm, norm}, s);
+            } else if (e == hipSuccess) {
                 e = ddp::launch_clip(norm_type, g->tables, g->clip_blocks, {max_norm, nullptr}, g->blocks, scratch,
                                      norm, s);
+            }
         }
         return e == hipSuccess ? int(DDP_OK) : hip_fail("gradient clipping", e);
     });
@@ -376,8 +387,9 @@ int ddp_clip_grads(const ddp_grads *g, float max_norm, const float *norm, void *
         if (rc == DDP_OK) rc = check_device(g, s);
         if (rc != DDP_OK) return rc;
         if (g->tables.all_tiles == 0) return int(DDP_OK);
-        const hipError_t e =
-            ddp::launch_clip(DDP_NORM_L2, g->tables, g->clip_blocks, {max_norm, norm}, 0, nullptr, nullptr, s);
+        const hipError_t e = g->parts ? ddp::launch_clip_parts(g->tables, {max_norm, norm}, s)
+                                      : ddp::launch_clip(DDP_NORM_L2, g->tables, g->clip_blocks, {max_norm, norm}, 0,
+                                                         nullptr, nullptr, s);
         return e == hipSuccess ? int(DDP_OK) : hip_fail("gradient clipping", e);
     });
 }

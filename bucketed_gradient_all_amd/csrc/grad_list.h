@@ -12,12 +12,21 @@ namespace ddp {
 // groups of four elements a thread: 32 KiB of fp32 in flight a workgroup.
 constexpr int kGradTile = 8192;
 
-// Lists of up to this many tiles are handled by one workgroup in one launch.
-constexpr int kSmallTiles = 6;
+// Lists of up to this many tiles are handled by one workgroup in one launch:
+// the norm, and the norm with clipping. Replayed from a graph, one launch
+// against two: the norm of 4 tiles 3.3 us against 4.7, of 12 5.4 against 4.9;
+// clipping of 4 tiles into another buffer 5.8 against 5.6, of 12 12.3 against
+// 5.7. Called one by one, the second launch costs the host about 3 us more.
+constexpr int kSmallNorm = 12, kSmallClip = 6;
 
 // Most workgroups the norm's pass is split over: each leaves one 8-byte
 // partial, and the last step sums them in index order.
-constexpr int kMaxPartials = 2048;
+constexpr int kMaxPartials = 1024;
+
+// Lists of more than this many tiles that are clipped into other buffers are
+// clipped by a workgroup a part of a tile, with the norm finished by a launch
+// of its own before.
+constexpr int kManyTiles = 4096;
 
 // One tensor of a list. Its tiles are cut at absolute destination addresses
 // that are multiples of 256 bytes, whatever address the tensor starts at, so
@@ -39,6 +48,7 @@ struct GradTables {
     const int32_t *tile_seg;   // tile -> tensor record
     int32_t norm_tiles;        // the first copy's tiles: what the norm is taken over
     int32_t all_tiles;         // every copy's: what clipping scales
+    int32_t in_place;          // clipping writes where it reads
 };
 
 // Where clipping takes the norm from.
@@ -55,6 +65,7 @@ hipError_t launch_norm_finish(int norm_type, int blocks, const void *partials, f
 // the first workgroup writes it to `norm`.
 hipError_t launch_clip(int norm_type, const GradTables &t, int blocks, const ClipFactor &f, int n_partials,
                        const void *partials, float *norm, hipStream_t s);
+hipError_t launch_clip_parts(const GradTables &t, const ClipFactor &f, hipStream_t s);
 // One workgroup: the norm, and with clip != 0 the scaling too.
 hipError_t launch_small(int norm_type, const GradTables &t, bool clip, float max_norm, float *norm, hipStream_t s);
 

@@ -67,6 +67,11 @@ hipError_t launch_clip(int, const GradTables &t, int, const ClipFactor &f, int, 
     g_tables = t;
     return note(f.norm ? "clip given" : "clip");
 }
+hipError_t launch_clip_parts(const GradTables &t, const ClipFactor &, hipStream_t)
+{
+    g_tables = t;
+    return note("clip parts");
+}
 hipError_t launch_small(int, const GradTables &t, bool clip, float, float *, hipStream_t)
 {
     g_tables = t;
@@ -201,14 +206,14 @@ void lists()
         const hipStream_t s = reinterpret_cast<hipStream_t>(uintptr_t(0x1000));
         expect(ddp_clip_grad_norm(g, DDP_NORM_L2, 1.0f, &norm, sc.at, scratch, s) == DDP_OK, name + ": clip");
         check_tables(d, ws.at, bytes, name);
-        const bool small = g_tables.all_tiles <= ddp::kSmallTiles;
+        const bool small = g_tables.all_tiles <= ddp::kSmallClip;
         auto l = launches();
         expect(l == (small ? std::vector<std::string>{"small clip"} : std::vector<std::string>{"partials", "clip"}),
                name + ": clip launches");
         if (!small) expect(size_t(g_blocks) * 8 <= scratch, name + ": partials past the scratch");
         expect(ddp_grad_norm(g, DDP_NORM_INF, &norm, sc.at, scratch, s) == DDP_OK, name + ": norm");
         l = launches();
-        expect(l.size() == (g_tables.norm_tiles <= ddp::kSmallTiles ? 1u : 2u), name + ": norm launches");
+        expect(l.size() == (g_tables.norm_tiles <= ddp::kSmallNorm ? 1u : 2u), name + ": norm launches");
         expect(ddp_clip_grads(g, 1.0f, &norm, s) == DDP_OK, name + ": given");
         l = launches();
         expect(l.size() == (g_tables.all_tiles ? 1u : 0u), name + ": given launches");

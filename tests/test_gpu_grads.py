@@ -142,8 +142,9 @@ LISTS = {
     "one": [1],
     "few": [1, 0, 2, 3, 5],
     "tile_edges": [8191, 8192, 8193, 127, 128, 129],
-    "small_edge": [6 * 8192 - 200],
+    "small_edge": [3 * 8192 - 200],
     "past_small": [7 * 8192, 17],
+    "norm_edge": [11 * 8192 - 200, 5],
     "mixed_sizes": [100003, 64, 1, 0, 30000, 8192 * 9 + 5],
     "many": [(i * 37) % 1100 for i in range(700)],
 }
@@ -181,6 +182,26 @@ def test_clip_over_types(name, types, apart):
         for vs in c.views:
             for v, x in zip(vs, c.values):
                 assert torch.equal(v.cpu(), x)
+
+
+@pytest.mark.parametrize("name,dtype,out", [("tensors", 0, 0), ("tensors", 1, 0), ("tensors", 1, 2), ("odd", 2, 1)])
+def test_clip_of_many_tiles_into_other_buffers(name, dtype, out):
+    """Past the size from which the clipping is a workgroup a part of a tile."""
+    torch, ddp = _torch(), _lib()
+    say("case many", name, dtype, out)
+    n = [(40 << 20) + 17, 1, 12345, 8192] if name == "tensors" else [9999 + i for i in range(2600)]
+    c = Case(n, [dtype] * len(n), out=[out] * len(n), seed=21, sigma=0.01)
+    norm = new_norm()
+    g = c.make()
+    s = torch.cuda.current_stream().cuda_stream
+    ddp.ddp_clip_grad_norm(g, 2, 0.5, norm.data_ptr(), s)
+    want = ref_norm(c.flat64(), 2)
+    check_norm(float(norm), want)
+    check_clip(c, want, 0.5)
+    c.guards_hold()
+    first = [v.clone() for v in c.out_views[0]]
+    ddp.ddp_clip_grads(g, 0.5, norm.data_ptr(), s)
+    assert all(torch.equal(a, b) for a, b in zip(first, c.out_views[0]))
 
 
 @pytest.mark.parametrize("kind", [0, 1, 2])
