@@ -630,6 +630,7 @@ class Grads:
         self.workspace = None                 # device allocations that live as long as the handle
         self.scratch = None
         self._scratch = (None, 0)
+        self._streams = None                  # streams those allocations know to be used on
 
     @property
     def handle(self):
@@ -638,6 +639,33 @@ class Grads:
     def set_scratch(self, ptr: int, nbytes: int) -> None:
         """The scratch of calls that are given none."""
         self._scratch = (ptr or None, nbytes)
+
+    def own(self, workspace, scratch) -> None:
+        """Keeps the torch allocations that hold the list's tables and its
+        scratch. The allocator learns of every stream they are used on, so that
+        memory of a handle dropped with calls still queued is not handed out
+        before these have run."""
+        import torch
+
+        self.workspace, self.scratch = workspace, scratch
+        self._streams = {torch.cuda.current_stream(workspace.device).cuda_stream}
+        self.set_scratch(scratch.data_ptr(), scratch.numel())
+
+    def used_on(self, stream: int) -> None:
+        if self._streams is None or stream in self._streams:
+            return
+        import torch
+
+        dev = self.workspace.device
+        # 1 names the null stream too; 2 is the calling thread's own stream,
+        # which the allocator does not take: a handle used on it has to live
+        # until its calls have run
+        if stream == 2:
+            return
+        s = torch.cuda.ExternalStream(stream, device=dev) if stream > 1 else torch.cuda.default_stream(dev)
+        self.workspace.record_stream(s)
+        self.scratch.record_stream(s)
+        self._streams.add(stream)
 
 
 def ddp_grads_create(desc: GradsDesc) -> Grads:
@@ -674,25 +702,36 @@ def ddp_grad_norm(g: Grads, norm_type: int, norm: int, stream: int, scratch: int
     """norm: device pointer of one float. Without a scratch the handle's own
     is used: then no other call of the handle may run at the same time."""
     p, n = (scratch, scratch_bytes) if scratch else g._scratch
+    g.used_on(stream)
     _check(g._lib.ddp_grad_norm(g.handle, norm_type, norm or None, p, n, stream or None), g._lib)
 
 
 def ddp_clip_grad_norm(g: Grads, norm_type: int, max_norm: float, norm: int, stream: int, scratch: int = 0,
                        scratch_bytes: int = 0) -> None:
     p, n = (scratch, scratch_bytes) if scratch else g._scratch
+    g.used_on(stream)
     _check(g._lib.ddp_clip_grad_norm(g.handle, norm_type, max_norm, norm or None, p, n, stream or None), g._lib)
 
 
 def ddp_clip_grads(g: Grads, max_norm: float, norm: int, stream: int) -> None:
+    g.used_on(stream)
     _check(g._lib.ddp_clip_grads(g.handle, max_norm, norm or None, stream or None), g._lib)
+
+
+def _idle_workspace(nbytes: int):
+    """A torch allocation that no queued work touches any more: the tables are
+    uploaded at once, and memory freed on the current stream may still be
+    written by kernels queued there."""
+    import torch
+
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    torch.cuda.current_stream().synchronize()
+    return ws
 
 
 def _with_scratch(g: Grads, ws) -> Grads:
     import torch
-    g.workspace = ws
-    n = ddp_grads_scratch_bytes(g)
-    g.scratch = torch.empty(n, dtype=torch.uint8, device=ws.device)
-    g.set_scratch(g.scratch.data_ptr(), n)
+    g.own(ws, torch.empty(ddp_grads_scratch_bytes(g), dtype=torch.uint8, device=ws.device))
     return g
 
 
@@ -701,21 +740,17 @@ def make_grads(numel: Sequence[int], grad_ptrs: Sequence[Sequence[int]], dtype: 
                out_dtype: Optional[Sequence[int]] = None) -> Grads:
     """Creates a gradient list on the current device; its workspace and a
     scratch are torch allocations that the returned handle keeps alive."""
-    import torch
-
     desc = GradsDesc(numel, grad_ptrs, dtype, out_ptrs, out_dtype)
     nbytes = ddp_grads_workspace_bytes(desc)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    ws = _idle_workspace(nbytes)
     desc.set_workspace(ws.data_ptr(), nbytes)
     return _with_scratch(ddp_grads_create(desc), ws)
 
 
 def make_reducer_grads(r: Reducer) -> Grads:
     """make_grads over a reducer's results (ddp_grads_from_reducer)."""
-    import torch
-
     nbytes = ddp_reducer_grads_workspace_bytes(r)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    ws = _idle_workspace(nbytes)
     return _with_scratch(ddp_grads_from_reducer(r, ws.data_ptr(), nbytes), ws)
 
 

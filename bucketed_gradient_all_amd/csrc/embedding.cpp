@@ -106,6 +106,11 @@ constexpr int64_t kSomeTokens = 16384, kManyTokens = 32768;
 // of the last cache it may still lie there from the kernel that wrote it.
 constexpr int64_t kStreamBytes = int64_t(64) << 20;
 
+// Waves side by side over a row's columns, and of the sum in all, at most:
+// what a launch's grid holds, 2^32 threads, with room for the rows that a whole
+// gradient fills.
+constexpr int64_t kMostSlabs = int64_t(1) << 20, kMostChunkWaves = int64_t(1) << 25;
+
 int64_t slabs_of(const ddp_embedding_desc &d)
 {
     return std::max<int64_t>(1, ceil_div(d.width, 64 * ddp::sum_vector(d.act_dtype, d.grad_dtype)));
@@ -166,9 +171,7 @@ int lookup(const ddp_embedding_desc *d, const void *table, const void *tokens, i
     if (rc == DDP_OK) rc = check_pointer("tokens", tokens, d->index_dtype == DDP_I64 ? 8 : 4);
     if (rc == DDP_OK) rc = check_pointer("out", out, element_size(d->act_dtype));
     if (rc != DDP_OK) return rc;
-    // one wave a row and 64 columns, at most
-    if (n * ceil_div(d->width, 64) > std::numeric_limits<int32_t>::max())
-        return fail(DDP_ERR_INVALID, "n_tokens times width is too large for one call");
+    if (ceil_div(d->width, 64) > kMostSlabs) return fail(DDP_ERR_INVALID, "width is too large for one call");
     rc = check_device(s);
     if (rc != DDP_OK) return rc;
     const hipError_t e = ddp::launch_lookup(args_of(*d, n), table, tokens, out, s);
@@ -204,14 +207,14 @@ int grad(const ddp_embedding_desc *d, const void *dout, const void *tokens, int6
     w.splits = n >= kManyTokens ? 4 : n >= kSomeTokens ? 2 : 1;
     w.sort_rows = int32_t(
         std::min<int64_t>(ddp::kMaxSortRows, std::max<int64_t>(16, ceil_div(d->n_rows, 256 / w.splits))));
-    w.stream = n * d->width * element_size(d->act_dtype) > kStreamBytes;
+    w.stream = n > kStreamBytes / (d->width * element_size(d->act_dtype));
     w.pad_row = -1;
     if (d->padding_idx >= 0 && d->padding_idx >= d->first_row &&
         uint64_t(d->padding_idx) - uint64_t(d->first_row) < uint64_t(d->n_rows))
         w.pad_row = int32_t(d->padding_idx - d->first_row);
     const int64_t wide = ceil_div(d->width, 64);   // slabs of the narrowest kernel, an upper bound
-    if ((w.n_chunks + (accumulate ? 0 : d->n_rows)) * wide > std::numeric_limits<int32_t>::max() - 8)
-        return fail(DDP_ERR_INVALID, "n_tokens and n_rows times width are too large for one call");
+    if (wide > kMostSlabs || w.n_chunks * wide > kMostChunkWaves)
+        return fail(DDP_ERR_INVALID, "n_tokens times width is too large for one call");
     rc = check_device(s);
     if (rc != DDP_OK) return rc;
     const EmbeddingArgs a = args_of(*d, n);
@@ -229,7 +232,7 @@ extern "C" {
 int ddp_embedding_lookup(const ddp_embedding_desc *desc, const void *table, const void *tokens, int64_t n_tokens,
                          void *out, void *stream)
 {
-    return guarded([&] { return lookup(desc, table, tokens, n_tokens, out, static_cast<hipStream_t>(stream)); });
+    return guarded([&] { return lookup(desc, table, tokens, n_tokens, out, ddp::stream_of(stream)); });
 }
 
 size_t ddp_embedding_grad_workspace_bytes(const ddp_embedding_desc *desc, int64_t n_tokens)
@@ -248,7 +251,7 @@ int ddp_embedding_grad(const ddp_embedding_desc *desc, const void *dout, const v
 {
     return guarded([&] {
         return grad(desc, dout, tokens, n_tokens, grad_out, accumulate != 0, workspace, workspace_bytes,
-                    static_cast<hipStream_t>(stream));
+                    ddp::stream_of(stream));
     });
 }
 

@@ -26,6 +26,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 namespace ddp {
 namespace {
 
@@ -142,6 +144,9 @@ __device__ __forceinline__ int row_of(const EmbeddingArgs &a, int64_t tok)
     return r < uint64_t(a.n_rows) ? int(r) : -1;
 }
 
+// Waves of a launch that covers rows of any number, at most.
+constexpr int64_t kMostWaves = int64_t(1) << 20;
+
 constexpr int kWaves = 4;   // of a workgroup of the row kernels
 
 __device__ __forceinline__ int wave_of()
@@ -161,29 +166,31 @@ template <int TABLE, int ACT, int VEC, int TOK>
 __global__ void __launch_bounds__(kLookupWaves * 64)
 lookup(EmbeddingArgs a, int slabs, const void *table, const void *tokens, void *out)
 {
-    const int64_t task = int64_t(blockIdx.x) * kLookupWaves + wave_of();
-    const int64_t group = task / slabs;
-    const int64_t t0 = group * TOK;
-    if (t0 >= a.n_tokens) return;
+    const int task = int(blockIdx.x) * kLookupWaves + wave_of();
+    const int groups = int(gridDim.x) * kLookupWaves / slabs;   // of rows that the launch works on at a time
+    const int group = task / slabs;
+    if (group >= groups) return;
     const Columns<VEC> c(task - group * slabs, int(threadIdx.x) % 64, a.width);
-    int row[TOK];
-    typename Raw<TABLE, VEC>::type x[TOK];
+    for (int64_t t0 = int64_t(group) * TOK; t0 < a.n_tokens; t0 += int64_t(groups) * TOK) {
+        int row[TOK];
+        typename Raw<TABLE, VEC>::type x[TOK];
 #pragma unroll
-    for (int k = 0; k < TOK; ++k) {
-        const int64_t t = min(t0 + k, a.n_tokens - 1);   // past the end: the last one again
-        row[k] = row_of(a, a.index64 ? ((const CONSTANT int64_t *)tokens)[t] : ((const CONSTANT int32_t *)tokens)[t]);
-    }
+        for (int k = 0; k < TOK; ++k) {
+            const int64_t t = min(t0 + k, a.n_tokens - 1);   // past the end: the last one again
+            row[k] = row_of(a, a.index64 ? ((const CONSTANT int64_t *)tokens)[t]
+                                         : ((const CONSTANT int32_t *)tokens)[t]);
+        }
 #pragma unroll
-    for (int k = 0; k < TOK; ++k)
-        if (row[k] >= 0) x[k] = load<TABLE, VEC>(table, row[k] * a.table_stride + c.col);
-    if (!c.on) return;
+        for (int k = 0; k < TOK; ++k)
+            if (row[k] >= 0) x[k] = load<TABLE, VEC>(table, row[k] * a.table_stride + c.col);
 #pragma unroll
-    for (int k = 0; k < TOK; ++k) {
-        if (t0 + k >= a.n_tokens) break;
-        float v[VEC];
+        for (int k = 0; k < TOK; ++k) {
+            if (!c.on || t0 + k >= a.n_tokens) break;
+            float v[VEC];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) v[j] = row[k] >= 0 ? __fmul_rn(a.scale, widen<TABLE>(x[k][j])) : 0.0f;
-        store<ACT, VEC>(out, (t0 + k) * a.act_stride + c.col, v, c.skip);
+            for (int j = 0; j < VEC; ++j) v[j] = row[k] >= 0 ? __fmul_rn(a.scale, widen<TABLE>(x[k][j])) : 0.0f;
+            store<ACT, VEC>(out, (t0 + k) * a.act_stride + c.col, v, c.skip);
+        }
     }
 }
 
@@ -434,7 +441,7 @@ __device__ __forceinline__ void arrive(T &v)
 // STREAM: dout is read past the caches.
 template <int ACT, int GRAD, int VEC, bool ACC, bool STREAM>
 __global__ void __launch_bounds__(kWaves * 64)
-sum_runs(EmbeddingArgs a, EmbeddingWork w, int slabs, int tasks, const void *dout, void *grad)
+sum_runs(EmbeddingArgs a, EmbeddingWork w, int slabs, int tasks, int fill_rows, const void *dout, void *grad)
 {
     constexpr int AHEAD = 8;
     const int task = int(blockIdx.x) * kWaves + wave_of();
@@ -443,12 +450,15 @@ sum_runs(EmbeddingArgs a, EmbeddingWork w, int slabs, int tasks, const void *dou
     if (task >= tasks) {
         // beyond the chunks: rows without a position, when the whole gradient
         // is written
-        const int64_t z = int64_t(task) - (tasks + kWaves - 1) / kWaves * kWaves;
-        const int64_t row = z / slabs;
-        if (ACC || z < 0 || row >= a.n_rows || (begin[row] != begin[row + 1] && row != w.pad_row)) return;
-        const Columns<VEC> c(z - row * slabs, lane, a.width);
+        const int z = task - (tasks + kWaves - 1) / kWaves * kWaves;
+        if (ACC || z < 0 || z >= fill_rows * slabs) return;
+        const int first = z / slabs;
+        const Columns<VEC> c(z - first * slabs, lane, a.width);
         const float none[VEC] = {};
-        if (c.on) store<GRAD, VEC>(grad, row * a.grad_stride + c.col, none, c.skip);
+        for (int64_t row = first; row < a.n_rows; row += fill_rows) {
+            if (begin[row] != begin[row + 1] && row != w.pad_row) continue;
+            if (c.on) store<GRAD, VEC>(grad, row * a.grad_stride + c.col, none, c.skip);
+        }
         return;
     }
     const int chunk = task / slabs;
@@ -639,7 +649,10 @@ hipError_t lookup_vec(const EmbeddingArgs &a, const void *table, const void *tok
     const int64_t slabs = slabs_of<VEC>(a.width);
     // four rows a wave once that leaves every CU sixteen waves
     const bool four = a.n_tokens * slabs >= 4 * 256 * 16;
-    const int64_t tasks = (four ? (a.n_tokens + kLookupRows - 1) / kLookupRows : a.n_tokens) * slabs;
+    const int64_t groups = four ? (a.n_tokens + kLookupRows - 1) / kLookupRows : a.n_tokens;
+    // a launch has a limited number of workgroups: beyond kMostWaves each goes
+    // on to further rows
+    const int64_t tasks = std::min(groups, std::max<int64_t>(1, kMostWaves / slabs)) * slabs;
     const dim3 g(static_cast<unsigned>((tasks + kLookupWaves - 1) / kLookupWaves)), b(kLookupWaves * 64);
     if (four)
         hipLaunchKernelGGL((lookup<TABLE, ACT, VEC, kLookupRows>), g, b, 0, s, a, int(slabs), table, tokens, out);
@@ -686,16 +699,17 @@ hipError_t sum_vec(const EmbeddingArgs &a, const void *dout, void *grad, bool ac
 {
     const int64_t slabs = slabs_of<VEC>(a.width);
     const int64_t tasks = w.n_chunks * slabs;
-    const int64_t fill = accumulate ? 0 : a.n_rows * slabs;
-    const int64_t blocks = (tasks + kWaves - 1) / kWaves + (fill + kWaves - 1) / kWaves;
+    // rows that are filled at a time: a wave goes on to further ones
+    const int64_t fill_rows = accumulate ? 0 : std::min(a.n_rows, std::max<int64_t>(1, kMostWaves / slabs));
+    const int64_t blocks = (tasks + kWaves - 1) / kWaves + (fill_rows * slabs + kWaves - 1) / kWaves;
     if (blocks == 0) return hipSuccess;
     const dim3 g(static_cast<unsigned>(blocks)), b(kWaves * 64);
     if (accumulate)
-        hipLaunchKernelGGL((sum_runs<ACT, GRAD, VEC, true, STREAM>), g, b, 0, s, a, w, int(slabs), int(tasks), dout,
-                           grad);
+        hipLaunchKernelGGL((sum_runs<ACT, GRAD, VEC, true, STREAM>), g, b, 0, s, a, w, int(slabs), int(tasks),
+                           int(fill_rows), dout, grad);
     else
-        hipLaunchKernelGGL((sum_runs<ACT, GRAD, VEC, false, STREAM>), g, b, 0, s, a, w, int(slabs), int(tasks), dout,
-                           grad);
+        hipLaunchKernelGGL((sum_runs<ACT, GRAD, VEC, false, STREAM>), g, b, 0, s, a, w, int(slabs), int(tasks),
+                           int(fill_rows), dout, grad);
     return hipGetLastError();
 }
 

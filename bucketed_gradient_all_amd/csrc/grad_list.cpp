@@ -30,6 +30,13 @@ namespace {
 
 constexpr size_t kAlign = 16;
 
+// Tiles of a list, at most: 2^41 elements.
+constexpr int64_t kMostTiles = int64_t(1) << 28;
+
+// Tiles of a list that is clipped by a workgroup a part of a tile, at most: a
+// launch's grid holds 2^32 threads.
+constexpr int64_t kMostPartTiles = int64_t(1) << 21;
+
 size_t align_up(size_t x)
 {
     return (x + kAlign - 1) / kAlign * kAlign;
@@ -70,7 +77,7 @@ int check_sizes(const ddp_grads_desc *d)
         if (!known_type(type_of(*d, i)) || !known_type(out_type_of(*d, i)))
             return fail(DDP_ERR_INVALID, "gradient " + std::to_string(i) + " has an unknown type");
         if (d->numel[i] > 0) tiles += d->numel[i] / kGradTile + 2;   // at most; the cut shifts them
-        if (tiles > std::numeric_limits<int32_t>::max() / d->n_copies)
+        if (tiles > kMostTiles / d->n_copies)
             return fail(DDP_ERR_INVALID, "the list has too many elements");
     }
     if (int64_t(d->n_tensors) * d->n_copies > std::numeric_limits<int32_t>::max())
@@ -179,7 +186,7 @@ int create(const ddp_grads_desc *d, ddp_grads **out)
     // tile pays. In place there is mostly nothing to do but to see that the
     // norm is below the bound, which 2048 workgroups do in 7 us; 41116, one a
     // tile, took 11.
-    g->parts = !g->tables.in_place && g->tables.all_tiles > ddp::kManyTiles;
+    g->parts = !g->tables.in_place && g->tables.all_tiles > ddp::kManyTiles && g->tables.all_tiles <= kMostPartTiles;
     *out = g.release();
     return DDP_OK;
 }
@@ -263,7 +270,9 @@ namespace ddp {
 
 int check_stream(hipStream_t s, int device)
 {
-    if (!s) return DDP_OK;   // the null stream is the current device's
+    // the null and the per-thread stream are the current device's (and the
+    // second is no object that could be asked)
+    if (!s || s == hipStreamPerThread) return DDP_OK;
     hipDevice_t of = -1;
     const hipError_t e = hipStreamGetDevice(s, &of);
     if (e != hipSuccess) return hip_fail("device of the stream", e);
@@ -337,7 +346,7 @@ int ddp_grad_norm(const ddp_grads *g, int32_t norm_type, float *norm, void *scra
                   void *stream)
 {
     return guarded([&] {
-        const hipStream_t s = static_cast<hipStream_t>(stream);
+        const hipStream_t s = ddp::stream_of(stream);
         const int rc = check_call(g, norm_type, norm, scratch, scratch_bytes, s);
         if (rc != DDP_OK) return rc;
         hipError_t e;
@@ -355,7 +364,7 @@ int ddp_clip_grad_norm(const ddp_grads *g, int32_t norm_type, float max_norm, fl
                        size_t scratch_bytes, void *stream)
 {
     return guarded([&] {
-        const hipStream_t s = static_cast<hipStream_t>(stream);
+        const hipStream_t s = ddp::stream_of(stream);
         int rc = check_call(g, norm_type, norm, scratch, scratch_bytes, s);
         if (rc == DDP_OK) rc = check_max_norm(max_norm);
         if (rc != DDP_OK) return rc;
@@ -379,7 +388,7 @@ int ddp_clip_grad_norm(const ddp_grads *g, int32_t norm_type, float max_norm, fl
 int ddp_clip_grads(const ddp_grads *g, float max_norm, const float *norm, void *stream)
 {
     return guarded([&] {
-        const hipStream_t s = static_cast<hipStream_t>(stream);
+        const hipStream_t s = ddp::stream_of(stream);
         if (!g) return fail(DDP_ERR_INVALID, "the gradient list is NULL");
         if (!norm || reinterpret_cast<uintptr_t>(norm) % 4)
             return fail(DDP_ERR_INVALID, "norm is NULL or misaligned");

@@ -33,6 +33,13 @@ int guarded(F &&body) noexcept
     }
 }
 
+// The stream of a call. hipStreamLegacy is another name of the null stream.
+inline hipStream_t stream_of(void *stream) noexcept
+{
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return s == hipStreamLegacy ? nullptr : s;
+}
+
 // DDP_OK if work on stream s runs on `device`, the current one. Defined in
 // grad_list.cpp.
 int check_stream(hipStream_t s, int device);

@@ -480,7 +480,9 @@ size_t ddp_grads_workspace_bytes(const ddp_grads_desc *desc);
 
 /* Builds the list's tables and uploads them (synchronously) into the
  * workspace, which must stay valid, as must the tensors, for as long as the
- * list is used. The list is tied to the device that is current here. *out is
+ * list, or a graph that recorded a call on it, is used. Not to be called while
+ * a stream is being recorded into a graph, nor with work queued that still
+ * touches the workspace. The list is tied to the device that is current here. *out is
  * set only on success.
  * Errors: DDP_ERR_INVALID: bad sizes, types or alignment; a tensor that
  * overlaps another (counted or scaled twice), or an `out` that overlaps any

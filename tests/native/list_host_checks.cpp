@@ -47,8 +47,10 @@ hipError_t note(const char *what)
 
 }  // namespace
 
-extern "C" hipError_t hipStreamGetDevice(hipStream_t, hipDevice_t *device)
+extern "C" hipError_t hipStreamGetDevice(hipStream_t s, hipDevice_t *device)
 {
+    // the runtime's own ends the process for these
+    expect(s && s != hipStreamLegacy && s != hipStreamPerThread, "a special stream handle was asked for its device");
     *device = g_stream_device;
     return hipSuccess;
 }
@@ -226,6 +228,9 @@ void lists()
             expect(ddp_clip_grad_norm(g, 2, bad, &norm, sc.at, scratch, s) == DDP_ERR_INVALID, name + ": bound");
             expect(ddp_clip_grads(g, bad, &norm, s) == DDP_ERR_INVALID, name + ": bound");
         }
+        for (hipStream_t special : {hipStream_t(nullptr), hipStreamLegacy, hipStreamPerThread})
+            expect(ddp_grad_norm(g, 2, &norm, sc.at, scratch, special) == DDP_OK, name + ": special stream");
+        launches();
         g_stream_device = 1;
         expect(ddp_grad_norm(g, 2, &norm, sc.at, scratch, s) == DDP_ERR_INVALID, name + ": other device");
         expect(ddp_clip_grad_norm(g, 2, 1.0f, &norm, sc.at, scratch, s) == DDP_ERR_INVALID, name + ": other device");
@@ -358,6 +363,9 @@ void embeddings()
         }
         expect(at <= ws + bytes, name + ": past the workspace");
         const hipStream_t s = reinterpret_cast<hipStream_t>(uintptr_t(0x1000));
+        for (hipStream_t special : {hipStream_t(nullptr), hipStreamLegacy, hipStreamPerThread})
+            expect(ddp_embedding_lookup(&d, p, p, n, p, special) == DDP_OK, name + ": special stream");
+        launches();
         g_stream_device = 1;
         expect(ddp_embedding_grad(&d, p, p, n, p, 1, ws, bytes, s) == DDP_ERR_INVALID, name + ": other device");
         expect(ddp_embedding_lookup(&d, p, p, n, p, s) == DDP_ERR_INVALID, name + ": other device");

@@ -446,3 +446,43 @@ def test_padding_between_other_rows_of_a_chunk(lead):
         c.host_tokens = tok
         c.tokens.copy_(tok)
         c.run_grad(accumulate)
+
+
+def test_more_rows_than_a_launch_has_waves():
+    """The lookup's and the filled rows' waves go on to further rows."""
+    torch, ddp = _torch(), _lib()
+    V, H, T = 1300003, 300, 4500001   # narrow rows: one wave a row, four rows a lookup's wave
+    say("case waves", V, H, T)
+    table = torch.arange(V, device="cuda", dtype=torch.float32)[:, None].expand(V, H).to(torch.bfloat16).contiguous()
+    tok = torch.randint(0, V, (T,), device="cuda")
+    out = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    d = ddp.EmbeddingDesc(V, H, table_dtype=1, grad_dtype=1, act_dtype=1)
+    s = torch.cuda.current_stream().cuda_stream
+    ddp.ddp_embedding_lookup(d, table.data_ptr(), tok.data_ptr(), T, out.data_ptr(), s)
+    for k in range(0, T, 500000):
+        assert torch.equal(out[k:k + 500000], table[tok[k:k + 500000]])
+    del table
+    few = 1000
+    dout = torch.ones(few, H, dtype=torch.bfloat16, device="cuda")
+    grad = torch.full((V, H), 3.0, dtype=torch.bfloat16, device="cuda")
+    n = ddp.ddp_embedding_grad_workspace_bytes(d, few)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    ddp.ddp_embedding_grad(d, dout.data_ptr(), tok.data_ptr(), few, grad.data_ptr(), False, ws.data_ptr(), n, s)
+    count = torch.bincount(tok[:few], minlength=V)
+    assert torch.equal(grad[:, 0].float(), count.float()) and torch.equal(grad[:, H - 1], grad[:, 0])
+    assert int(grad.count_nonzero()) == int(count.count_nonzero()) * H
+
+
+@pytest.mark.parametrize("stream", [0, 1, 2])
+def test_the_null_the_legacy_and_the_per_thread_stream(stream):
+    """Streams with names of their own: hipStreamLegacy is 1, hipStreamPerThread 2."""
+    torch, ddp = _torch(), _lib()
+    c = Case(3000, 40, 30, kind="falling", seed=31)
+    before = c.row.cpu().clone()
+    n = ddp.ddp_embedding_grad_workspace_bytes(c.desc, c.T)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    ddp.ddp_embedding_grad(c.desc, c.act.data_ptr(), c.tokens.data_ptr(), c.T, c.row.data_ptr(), True, ws.data_ptr(), n,
+                           stream)
+    torch.cuda.synchronize()
+    c.check_grad(before, True)

@@ -448,3 +448,23 @@ def test_list_refusals_on_the_device():
     ddp.ddp_grads_destroy(g)
     with pytest.raises(ddp.DDPError):
         ddp.ddp_grad_norm(g, 2, norm.data_ptr(), s)
+
+
+def test_a_handle_dropped_with_its_calls_queued_on_another_stream():
+    """The memory of its tables is not handed out before they have run."""
+    torch, ddp = _torch(), _lib()
+    c = Case([20000003], copies=2, out=[1], seed=15)
+    side = torch.cuda.Stream()
+    norms = [new_norm() for _ in range(8)]
+    torch.cuda.synchronize()
+    for x in norms:
+        ddp.ddp_clip_grad_norm(c.make(), 2, 0.5, x.data_ptr(), side.cuda_stream)
+        for _ in range(4):   # takes what the allocator thinks free, on the stream it was allocated on
+            torch.full((400000,), 255, dtype=torch.uint8, device="cuda")
+            torch.full((30000,), 255, dtype=torch.uint8, device="cuda")
+            torch.full((8192,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    want = ref_norm(c.flat64(), 2)
+    for x in norms:
+        check_norm(float(x), want)
+    check_clip(c, want, 0.5)

@@ -158,9 +158,9 @@ def test_embedding_pointers_are_checked():
 def test_embedding_calls_too_large_for_a_launch_are_refused():
     wide = _desc(n_rows=10, width=(1 << 31) - 1)
     _refused(lambda: ddp.ddp_embedding_lookup(wide, A, B, 100, WS, 0), "too large")
-    _refused(lambda: ddp.ddp_embedding_grad(wide, A, B, 10000, A, True, WS, 1 << 62, 0), "too large")
-    tall = _desc(n_rows=(1 << 31) - 2, width=128)
-    _refused(lambda: ddp.ddp_embedding_grad(tall, A, B, 1, A, False, WS, 1 << 62, 0), "too large")
+    _refused(lambda: ddp.ddp_embedding_grad(wide, A, B, 1, A, True, WS, 1 << 62, 0), "too large")
+    long = _desc(n_rows=10, width=1 << 20)
+    _refused(lambda: ddp.ddp_embedding_grad(long, A, B, 1 << 30, A, True, WS, 1 << 62, 0), "too large")
 
 
 def test_embedding_calls_with_nothing_to_do_touch_no_device():
