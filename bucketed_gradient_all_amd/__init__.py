@@ -64,8 +64,10 @@ HIPCC_FLAGS = ["--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17",
 
 # one object per source; the kernel families compile in parallel
 SOURCES = ["reducer.cpp", "grad_list.cpp", "embedding.cpp", "bucket_reduce.hip", "bucket_bf16_hook.hip",
-           "bucket_fp16_hook.hip", "static_tables.hip", "grad_norm.hip", "embedding.hip"]
-HEADERS = ["host_common.h", "internal.h", "reduce_kernels.h", "static_area.h", "grad_list.h", "embedding.h"]
+           "bucket_fp16_hook.hip", "static_tables.hip", "grad_norm.hip", "embedding.hip",
+           "embedding_small.hip"]
+HEADERS = ["host_common.h", "internal.h", "reduce_kernels.h", "static_area.h", "grad_list.h", "embedding.h",
+           "embedding_kernels.h"]
 
 
 BUILD_DIR = os.path.join(HERE, "_build")

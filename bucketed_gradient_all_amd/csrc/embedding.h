@@ -48,6 +48,19 @@ struct EmbeddingWork {
     int32_t pad_row;     // the row whose positions count for nothing, or -1
 };
 
+// A small batch's gradient in one launch: positions it takes at most (an entry
+// holds a position in 16 bits, a wave four groups of 64 tokens), and rows of a
+// workgroup's range (one a thread).
+constexpr int kSmallTokens = 4096, kSmallRows = 1024;
+
+struct SmallPlan {
+    int32_t rows;      // of a workgroup's range
+    int32_t slabs;     // of columns
+    int32_t pad_row;   // the row whose positions count for nothing, or -1
+};
+
+hipError_t launch_small_grad(const EmbeddingArgs &a, const SmallPlan &p, const void *tokens, const void *dout,
+                             void *grad, bool accumulate, hipStream_t s);
 hipError_t launch_lookup(const EmbeddingArgs &a, const void *table, const void *tokens, void *out, hipStream_t s);
 hipError_t launch_sort(const EmbeddingArgs &a, const void *tokens, const EmbeddingWork &w, hipStream_t s);
 hipError_t launch_sum(const EmbeddingArgs &a, const void *dout, void *grad, bool accumulate, const EmbeddingWork &w,

@@ -33,6 +33,7 @@ std::vector<std::string> g_launches;
 ddp::GradTables g_tables;
 int g_blocks = 0;
 ddp::EmbeddingWork g_work;
+ddp::SmallPlan g_small;
 
 void expect(bool ok, const std::string &what)
 {
@@ -78,6 +79,12 @@ hipError_t launch_small(int, const GradTables &t, bool clip, float, float *, hip
 {
     g_tables = t;
     return note(clip ? "small clip" : "small");
+}
+hipError_t launch_small_grad(const EmbeddingArgs &, const SmallPlan &p, const void *, const void *, void *, bool,
+                             hipStream_t)
+{
+    g_small = p;
+    return note("small grad");
 }
 hipError_t launch_lookup(const EmbeddingArgs &, const void *, const void *, void *, hipStream_t)
 {
@@ -319,15 +326,19 @@ void reducers()
 void embeddings()
 {
     std::mt19937 rng(11);
+    int small_calls = 0, large_calls = 0;
     for (int round = 0; round < 300; ++round) {
         ddp_embedding_desc d{};
         d.n_rows = 1 + int64_t(rng() % (round % 3 ? 3000 : 900000));
         d.width = 1 + int64_t(rng() % 5000);
         d.table_stride = d.grad_stride = d.act_stride = d.width;
         d.scale = 1.0f;
-        d.padding_idx = -1;
+        d.first_row = int64_t(rng() % 2) * 1000;
+        d.padding_idx = int64_t(rng() % 3000) - 1;
+        if (d.padding_idx < d.first_row || d.padding_idx >= d.first_row + d.n_rows) d.padding_idx = -1;
         d.index_dtype = DDP_I64;
         d.act_dtype = int32_t(rng() % 3);
+        d.grad_dtype = int32_t(rng() % 3);
         const int64_t n = 1 + int64_t(rng() % (round % 2 ? 100 : 60000));
         const std::string name = "embedding " + std::to_string(round);
         const size_t bytes = ddp_embedding_grad_workspace_bytes(&d, n + int64_t(rng() % 5000));
@@ -337,6 +348,20 @@ void embeddings()
         expect(ddp_embedding_grad(&d, p, p, n, p, 1, ws, bytes, nullptr) == DDP_OK, name + ": " + ddp_last_error());
         const ddp::EmbeddingWork &w = g_work;
         const auto l = launches();
+        const int vec = ddp::sum_vector(d.act_dtype, d.grad_dtype);
+        if (l == std::vector<std::string>{"small grad"}) {
+            const ddp::SmallPlan &q = g_small;
+            expect(n <= ddp::kSmallTokens && d.width >= vec, name + ": small path taken for a large call");
+            expect(q.rows >= 1 && q.rows <= ddp::kSmallRows, name + ": rows of a small range");
+            expect(int64_t(q.slabs) * 64 * vec >= d.width && int64_t(q.slabs - 1) * 64 * vec < d.width,
+                   name + ": slabs of the small path");
+            const int64_t lds = 4 * (17 * int64_t(q.rows) + 1 + n + 16 * 64 * vec);
+            expect(lds + 1024 <= 160 * 1024, name + ": LDS of the small path");
+            expect(q.pad_row == -1 || q.pad_row == d.padding_idx - d.first_row, name + ": padding row");
+            ++small_calls;
+            continue;
+        }
+        ++large_calls;
         std::vector<std::string> want = {"sort", "sum"};
         if (n > w.chunk) want.push_back("join");
         expect(l == want, name + ": launches");
@@ -371,6 +396,7 @@ void embeddings()
         expect(ddp_embedding_lookup(&d, p, p, n, p, s) == DDP_ERR_INVALID, name + ": other device");
         expect(launches().empty(), name + ": a refused call launched");
     }
+    expect(small_calls >= 20 && large_calls >= 20, "embeddings: one path hardly taken");
 }
 
 void exhaustion()

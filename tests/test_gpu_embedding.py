@@ -290,19 +290,42 @@ def test_padding_contributes_nothing(accumulate):
     c.run_grad(accumulate)
 
 
-def test_runs_at_every_place_of_a_chunk():
+# Tables of so many rows take the path of several launches whatever the number
+# of positions; small ones the one of a single launch for few positions.
+FEW, MANY = 64, 600000
+
+
+@pytest.mark.parametrize("V", [FEW, MANY])
+@pytest.mark.parametrize("lead", range(9))
+def test_runs_at_every_place_of_a_chunk(V, lead):
     """Runs of every length up to past two chunks, one after the other, so that
-    they begin and end everywhere in the chunks."""
+    they begin and end everywhere in the chunks, and in the waves' parts."""
     torch = _torch()
-    lengths = [n for n in range(1, 21)] + [17, 16, 15, 9, 8, 7, 1, 1, 33, 8, 24, 16, 8]
+    lengths = [n for n in range(1, 21)] + [17, 16, 15, 9, 8, 7, 1, 1, 33, 8, 24, 16, 8, 70, 64, 65, 130]
     t = torch.cat([torch.full((n,), i) for i, n in enumerate(lengths)])
-    for lead in range(9):
-        tok = torch.cat([torch.zeros(lead, dtype=torch.long), t + 1])
-        tok = tok[torch.randperm(tok.numel(), generator=torch.Generator().manual_seed(lead))]
-        c = Case(tok.numel(), len(lengths) + 1, 16, seed=lead)
+    tok = torch.cat([torch.zeros(lead, dtype=torch.long), t + 1]) * (V // 64)
+    tok = tok[torch.randperm(tok.numel(), generator=torch.Generator().manual_seed(lead))]
+    for accumulate in (True, False):
+        c = Case(tok.numel(), V, 16, seed=lead)
         c.host_tokens = tok
         c.tokens.copy_(tok)
-        c.run_grad(True)
+        c.run_grad(accumulate)
+
+
+@pytest.mark.parametrize("T", [1, 2, 9, 63, 65, 1000, 3000])
+@pytest.mark.parametrize("kind", ["uniform", "same", "falling", "wild", "two"])
+def test_gradient_of_few_tokens_in_a_large_table(T, kind):
+    say("case grad large table", T, kind)
+    Case(T, MANY, 20, kind=kind, scale=1.3, first=7, padding=9, seed=T).run_grad(True)
+
+
+@pytest.mark.parametrize("V,H,act,row", [(32000, 2048, 1, 0), (32000, 2048, 1, 1), (30522, 1024, 0, 0), (200, 4099, 2, 2),
+                                         (130000, 300, 1, 0), (5, 130, 0, 1)])
+@pytest.mark.parametrize("T", [1, 500, 2047, 4096, 4097])
+@pytest.mark.parametrize("kind", ["falling", "same"])
+def test_gradient_of_few_tokens(V, H, act, row, T, kind):
+    say("case grad few", V, H, act, row, T, kind)
+    Case(T, V, H, kind=kind, act=act, row=row, scale=0.7, padding=1, seed=T + V).run_grad(True)
 
 
 def test_one_row_for_every_position():
@@ -434,15 +457,16 @@ def test_two_gradients_at_once_on_two_streams():
         c.check_grad(b, True)
 
 
+@pytest.mark.parametrize("V", [FEW, MANY])
 @pytest.mark.parametrize("lead", range(20))
-def test_padding_between_other_rows_of_a_chunk(lead):
+def test_padding_between_other_rows_of_a_chunk(V, lead):
     """The padding row's positions lie between other rows' in the sorted order,
     at every offset from the chunks' borders."""
     torch = _torch()
     tok = torch.cat([torch.arange(lead), torch.full((5 + lead,), 30), torch.arange(31, 60), torch.full((40,), 61)])
-    tok = tok[torch.randperm(tok.numel(), generator=torch.Generator().manual_seed(lead))]
+    tok = tok[torch.randperm(tok.numel(), generator=torch.Generator().manual_seed(lead))] * (V // 64)
     for accumulate in (True, False):
-        c = Case(tok.numel(), 64, 24, padding=30, seed=lead)
+        c = Case(tok.numel(), V, 24, padding=30 * (V // 64), seed=lead)
         c.host_tokens = tok
         c.tokens.copy_(tok)
         c.run_grad(accumulate)
