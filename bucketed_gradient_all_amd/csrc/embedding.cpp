@@ -97,11 +97,6 @@ int check_device(hipStream_t s)
 // Waves that share the positions of the sum, at most, before chunks grow.
 constexpr int64_t kWantedWaves = 8192;
 
-// Positions from which a range of rows is sorted by two, and by four
-// workgroups. 8191 positions of 32000 rows: 9.2 us with one, 9.4 with two, 12.1
-// with four; 32768: 21.6, 16.6, 15.0 (eight: 21.2).
-constexpr int64_t kSomeTokens = 16384, kManyTokens = 32768;
-
 // Bytes of dout from which it is read past the caches: well below the 256 MiB
 // of the last cache it may still lie there from the kernel that wrote it.
 constexpr int64_t kStreamBytes = int64_t(64) << 20;
@@ -158,6 +153,24 @@ Layout layout_of(const ddp_embedding_desc &d, int64_t n_tokens)
     l.more = take(slots);
     l.total = cur;
     return l;
+}
+
+// Positions for which another workgroup shares a range's sorting: 32000 rows,
+// 8191 positions 9.2 us with one, 9.4 with two, 12.1 with four; 32768 positions
+// 21.6, 16.6, 15.0 (eight: 21.2); 262144 positions 67 with four, 60 with eight,
+// 58 with sixteen.
+constexpr int64_t kSplitTokens = 8192;
+
+// The sort's workgroups: about 256, one a CU, are ranges of rows, as far as a
+// range's counters fit the LDS, times the workgroups of a range.
+void sort_plan(const ddp_embedding_desc &d, int64_t n, EmbeddingWork *w)
+{
+    const int64_t fewest = ceil_div(d.n_rows, ddp::kMaxSortRows);   // ranges
+    const int64_t splits =
+        std::max<int64_t>(1, std::min({int64_t(64), n / kSplitTokens, 256 / std::max<int64_t>(1, fewest)}));
+    w->sort_rows =
+        int32_t(std::min<int64_t>(ddp::kMaxSortRows, std::max<int64_t>(16, ceil_div(d.n_rows, 256 / splits))));
+    w->splits = int32_t(splits);
 }
 
 // Bytes of dout that one workgroup of the one-launch path may have to read, if
@@ -233,11 +246,7 @@ int grad(const ddp_embedding_desc *d, const void *dout, const void *tokens, int6
     w.pitch = l.pitch;
     w.chunk = chunk_of(*d, n);
     w.n_chunks = int32_t(ceil_div(n, w.chunk));
-    // about 256 workgroups, one a CU: ranges of rows, as far as a range's
-    // counters fit the LDS, times the workgroups of a range
-    w.splits = n >= kManyTokens ? 4 : n >= kSomeTokens ? 2 : 1;
-    w.sort_rows = int32_t(
-        std::min<int64_t>(ddp::kMaxSortRows, std::max<int64_t>(16, ceil_div(d->n_rows, 256 / w.splits))));
+    sort_plan(*d, n, &w);
     w.stream = n > kStreamBytes / (d->width * element_size(d->act_dtype));
     w.pad_row = pad_row_of(*d);
     const int64_t wide = ceil_div(d->width, 64);   // slabs of the narrowest kernel, an upper bound

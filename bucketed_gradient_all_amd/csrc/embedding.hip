@@ -385,8 +385,11 @@ sum_runs(EmbeddingArgs a, EmbeddingWork w, int slabs, int tasks, int fill_rows, 
 // ---------------------------------------------------------------- join
 // A workgroup looks after the long runs that begin in kJoinChunks chunks, over
 // a slab of columns. Runs of few pieces go one to a wave; the pieces of one of
-// many are split over the four waves and the waves' sums added in order.
-constexpr int kJoinChunks = 8;
+// many are split over the waves and the waves' sums added in order. 16 waves
+// and 16 chunks: 65536 positions of 64 columns 6.5 us, of two tokens alone 15.6;
+// with 4 waves and 8 chunks 11.1 and 34, but where there is little to join 0.3
+// to 1.6 us less.
+constexpr int kJoinChunks = 16, kJoinWaves = 16;
 constexpr int kFewPieces = 16;
 
 // Pieces [k, to) of a long run.
@@ -409,9 +412,9 @@ __device__ __forceinline__ void add_pieces(const EmbeddingWork &w, const Columns
 }
 
 template <int GRAD, int VEC, bool ACC>
-__global__ void __launch_bounds__(kWaves * 64) join_runs(EmbeddingArgs a, EmbeddingWork w, int slabs, void *grad)
+__global__ void __launch_bounds__(kJoinWaves * 64) join_runs(EmbeddingArgs a, EmbeddingWork w, int slabs, void *grad)
 {
-    __shared__ float part[kWaves][VEC][64];
+    __shared__ float part[kJoinWaves][VEC][64];
     const int group = int(blockIdx.x) / slabs, slab = int(blockIdx.x) - group * slabs;
     const int wave = wave_of(), lane = int(threadIdx.x) % 64;
     const CONSTANT int32_t *begin = (const CONSTANT int32_t *)w.begin;
@@ -432,7 +435,7 @@ __global__ void __launch_bounds__(kWaves * 64) join_runs(EmbeddingArgs a, Embedd
         const int k = __ffsll((unsigned long long)many) - 1;
         const int n = __builtin_amdgcn_readlane(pieces, k), first = group * kJoinChunks + k;
         const int64_t r = __builtin_amdgcn_readlane(row, k);
-        const int each = (n + kWaves - 1) / kWaves;
+        const int each = (n + kJoinWaves - 1) / kJoinWaves;
         float sum[VEC] = {};
         add_pieces<VEC>(w, c, first + 1 + wave * each, min(first + 1 + n, first + 1 + (wave + 1) * each), sum);
 #pragma unroll
@@ -446,14 +449,14 @@ __global__ void __launch_bounds__(kWaves * 64) join_runs(EmbeddingArgs a, Embedd
             for (int e = 0; e < VEC; ++e) {
                 sum[e] = x[e];
 #pragma unroll
-                for (int v = 0; v < kWaves; ++v) sum[e] = __fadd_rn(sum[e], part[v][e][lane]);
+                for (int v = 0; v < kJoinWaves; ++v) sum[e] = __fadd_rn(sum[e], part[v][e][lane]);
             }
             put<GRAD, VEC, ACC>(a, grad, int(r), c, old, sum);
         }
         __syncthreads();
     }
     for (int turn = 0; few; few &= few - 1, ++turn) {
-        if (turn % kWaves != wave) continue;
+        if (turn % kJoinWaves != wave) continue;
         const int k = __ffsll((unsigned long long)few) - 1;
         const int n = __builtin_amdgcn_readlane(pieces, k), first = group * kJoinChunks + k;
         const int64_t r = __builtin_amdgcn_readlane(row, k);
@@ -563,7 +566,7 @@ template <int GRAD, int VEC>
 hipError_t join_vec(const EmbeddingArgs &a, void *grad, bool accumulate, const EmbeddingWork &w, hipStream_t s)
 {
     const int64_t slabs = slabs_of<VEC>(a.width);
-    const dim3 g(static_cast<unsigned>((w.n_chunks + kJoinChunks - 1) / kJoinChunks * slabs)), b(kWaves * 64);
+    const dim3 g(static_cast<unsigned>((w.n_chunks + kJoinChunks - 1) / kJoinChunks * slabs)), b(kJoinWaves * 64);
     if (accumulate)
         hipLaunchKernelGGL((join_runs<GRAD, VEC, true>), g, b, 0, s, a, w, int(slabs), grad);
     else

@@ -270,7 +270,9 @@ def test_gradient_types_and_addresses(row, act, index64, shift, extra, accumulat
 
 @pytest.mark.parametrize("T,V,H,kind", [(40000, 300, 64, "falling"), (40000, 32000, 513, "falling"),
                                         (70000, 7, 20, "uniform"), (33000, 1000, 2048, "same"),
-                                        (200000, 50000, 8, "two"), (20000, 2, 3, "uniform")])
+                                        (200000, 50000, 8, "two"), (20000, 2, 3, "uniform"),
+                                        (600000, 300, 4, "falling"), (530000, 3000, 5, "uniform"),
+                                        (140000, 400000, 4, "falling"), (70001, 1, 33, "same")])
 @pytest.mark.parametrize("accumulate", [True, False])
 def test_gradient_long_runs(T, V, H, kind, accumulate):
     say("case grad long", T, V, H, kind, accumulate)
