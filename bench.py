@@ -604,6 +604,8 @@ def main():
                     help="synthetic backward: a one-workgroup wait, or bf16 GEMMs that compete for the GPU")
     ap.add_argument("--workgroups-per-cu", type=int, default=0,
                     help="reduction workgroups per CU (0: the library's automatic choice, -1: no cap)")
+    ap.add_argument("--clip-norm", type=float, default=0.0,
+                    help="also time the step followed by the gradients' norm and clipping to this bound (0: not)")
     ap.add_argument("--sweep", action="store_true", help="run the bucket-size sweep instead of one workload")
     ap.add_argument("--sweep-worlds", default="2,4,8,16,32")
     ap.add_argument("--sweep-caps", default="0,1,5,10,25,50,100,200")
@@ -774,6 +776,33 @@ def main():
                 "overlap_gain_ms": round((t_se - t_ov) * 1e3, 3),
                 "reduce_ms_alone": round(step_s * 1e3, 3)}
 
+    # the step followed by the norm of the reduced gradients and their clipping
+    # on the compute stream, as a training step goes on after ddp_finish
+    clip = None
+    if args.clip_norm > 0:
+        grads = ddp.make_reducer_grads(s.r)
+        norm = torch.zeros((), dtype=torch.float32, device="cuda")
+
+        def clip_once():
+            ddp.ddp_clip_grad_norm(grads, ddp.DDP_NORM_L2, args.clip_norm, norm.data_ptr(), s.compute.cuda_stream)
+
+        def timed_clip(with_step):
+            torch.cuda.synchronize()
+            t0 = time.perf_counter()
+            for _ in range(args.steps):
+                if with_step:
+                    s.step()
+                clip_once()
+            torch.cuda.synchronize()
+            return (time.perf_counter() - t0) / args.steps
+
+        timed_clip(True)
+        t_both = timed_clip(True)
+        first_norm = float(norm)
+        clip = {"max_norm": args.clip_norm, "norm": first_norm, "step_and_clip_ms": round(t_both * 1e3, 4),
+                "clip_below_bound_ms": round(timed_clip(False) * 1e3, 4)}
+        ddp.ddp_grads_destroy(grads)
+
     overlap = overlap_gemm = None
     if args.backward_ms > 0:
         # a backward that takes no resources (a one-workgroup wait), and one
@@ -860,6 +889,7 @@ def main():
                                                 if scrubbed is not None else None)},
         "per_bucket_launch": per_bucket_launch,
         "graph_replay": graph_replay,
+        "clip": clip,
         "overlap": overlap,
         "overlap_gemm_backward": overlap_gemm,
         "plain_layout": plain,

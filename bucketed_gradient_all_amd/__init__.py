@@ -623,7 +623,9 @@ def _release_grads(holder: list, L) -> None:
 
 
 class Grads:
-    """Handle of a ddp_grads, and the scratch its calls use by default."""
+    """Handle of a ddp_grads, and the scratch its calls use by default. A graph
+    that recorded a call reads the handle's tables at every replay: keep the
+    handle as long."""
 
     def __init__(self, handle: int):
         self._holder = [handle]
@@ -702,7 +704,8 @@ def ddp_grads_scratch_bytes(g: Grads) -> int:
 
 def ddp_grad_norm(g: Grads, norm_type: int, norm: int, stream: int, scratch: int = 0, scratch_bytes: int = 0) -> None:
     """norm: device pointer of one float. Without a scratch the handle's own
-    is used: then no other call of the handle may run at the same time."""
+    is used: then no other call of the handle, nor a replay of one, may run at
+    the same time."""
     p, n = (scratch, scratch_bytes) if scratch else g._scratch
     g.used_on(stream)
     _check(g._lib.ddp_grad_norm(g.handle, norm_type, norm or None, p, n, stream or None), g._lib)

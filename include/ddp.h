@@ -482,8 +482,8 @@ size_t ddp_grads_workspace_bytes(const ddp_grads_desc *desc);
  * workspace, which must stay valid, as must the tensors, for as long as the
  * list, or a graph that recorded a call on it, is used. Not to be called while
  * a stream is being recorded into a graph, nor with work queued that still
- * touches the workspace. The list is tied to the device that is current here. *out is
- * set only on success.
+ * touches the workspace. The list is tied to the device that is current here.
+ * *out is set only on success.
  * Errors: DDP_ERR_INVALID: bad sizes, types or alignment; a tensor that
  * overlaps another (counted or scaled twice), or an `out` that overlaps any
  * tensor or another `out`; DDP_ERR_HIP; DDP_ERR_NOMEM. */
@@ -576,8 +576,7 @@ typedef struct {
 } ddp_embedding_desc;
 
 /* out[t] = R(scale * table[tokens[t] - first_row]) for t in [0, n_tokens),
- * n_tokens in [0, 2^30], 0
- * for an index the table does not hold: the product in fp32, R one rounding to
+ * n_tokens in [0, 2^30]; 0 for an index the table does not hold: the product in fp32, R one rounding to
  * act_dtype. All pointers are device memory at multiples of their element's
  * size; out must overlap neither table nor tokens. Elements of out between
  * the rows are left alone. May be recorded into a HIP graph.
@@ -593,15 +592,15 @@ int ddp_embedding_lookup(const ddp_embedding_desc *desc, const void *table, cons
 size_t ddp_embedding_grad_workspace_bytes(const ddp_embedding_desc *desc, int64_t n_tokens);
 
 /* grad[v] (+)= scale * sum of dout[t] over the positions t whose token is row
- * v's, in position order: with accumulate != 0 the sum is added to what grad
- * holds and rows without a position are not touched; with accumulate == 0
- * grad's old contents are not read and rows without a position become 0. Sums
+ * v's: with accumulate != 0 the sum is added to what grad holds and rows
+ * without a position are not touched; with accumulate == 0 grad's old contents are not read and rows without a position become 0. Sums
  * are fp32, rounded once to grad_dtype. The order of the additions depends on
- * the tokens alone: the same call gives the same bits every time (no
- * floating-point atomics).
+ * the sizes and the tokens alone: the same call gives the same bits every time
+ * (no floating-point atomics). dout is not read at positions that do not count.
  * The positions are sorted by token first (stable), then each row's are summed
- * once. All pointers are device memory at multiples of their element's size
- * (workspace: 256 bytes); grad must overlap no other argument. A workspace
+ * once, a frequent token's in pieces that are added in order. All pointers are
+ * device memory at multiples of their element's size (workspace: 256 bytes);
+ * grad must overlap no other argument. A workspace
  * serves one call at a time: calls that may run at once, replays of captured
  * ones included, need one each. May be recorded into a HIP graph.
  * Errors: as ddp_embedding_lookup; DDP_ERR_INVALID for a missing or too small

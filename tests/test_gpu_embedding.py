@@ -512,3 +512,33 @@ def test_the_null_the_legacy_and_the_per_thread_stream(stream):
                            stream)
     torch.cuda.synchronize()
     c.check_grad(before, True)
+
+
+@pytest.mark.parametrize("T,V", [(900, 50), (20000, 50), (900, 600000)])
+@pytest.mark.parametrize("act", [0, 1])
+def test_nan_in_places_that_do_not_count(T, V, act):
+    """Rows of dout at padding positions and at indices outside the table are
+    NaN or infinite, and so are rows of the table that no token names."""
+    torch = _torch()
+    for accumulate in (True, False):
+        c = Case(T, V, 24, kind="wild", act=act, padding=V // 2, first=0, seed=T + V)
+        r = c.host_tokens
+        c.host_tokens = torch.where(torch.arange(T) % 3 == 0, torch.full_like(r, V // 2), r)
+        c.tokens.copy_(c.host_tokens)
+        out = (c.host_tokens < 0) | (c.host_tokens >= V) | (c.host_tokens == V // 2)
+        c.act[out.cuda()] = math.nan
+        c.act[(out & (torch.arange(T) % 2 == 0)).cuda()] = math.inf
+        before = c.row.cpu().clone()
+        c.grad(accumulate)
+        assert bool(torch.isfinite(c.row).all())
+        clean = c.act.clone()
+        c.act[out.cuda()] = 0.0   # for the reference, which leaves them out by the mask
+        c.check_grad(before, accumulate)
+        del clean
+    c = Case(T, V, 24, kind="wild", act=act, seed=1)
+    named = torch.zeros(V, dtype=torch.bool)
+    held = (c.host_tokens >= 0) & (c.host_tokens < V)
+    named[c.host_tokens[held]] = True
+    c.row[(~named).cuda()] = math.nan
+    c.lookup()
+    c.check_lookup()
