@@ -41,30 +41,28 @@ __global__ void __launch_bounds__(kLookupWaves * 64)
 lookup(EmbeddingArgs a, int slabs, const void *table, const void *tokens, void *out)
 {
     const int task = int(blockIdx.x) * kLookupWaves + wave_of();
-    const int groups = int(gridDim.x) * kLookupWaves / slabs;   // of rows that the launch works on at a time
     const int group = task / slabs;
-    if (group >= groups) return;
+    const int64_t t0 = int64_t(group) * TOK;
+    if (t0 >= a.n_tokens) return;
     const Columns<VEC> c(task - group * slabs, int(threadIdx.x) % 64, a.width);
-    for (int64_t t0 = int64_t(group) * TOK; t0 < a.n_tokens; t0 += int64_t(groups) * TOK) {
-        int row[TOK];
-        typename Raw<TABLE, VEC>::type x[TOK];
+    int row[TOK];
+    typename Raw<TABLE, VEC>::type x[TOK];
 #pragma unroll
-        for (int k = 0; k < TOK; ++k) {
-            const int64_t t = min(t0 + k, a.n_tokens - 1);   // past the end: the last one again
-            row[k] = row_of(a, a.index64 ? ((const CONSTANT int64_t *)tokens)[t]
-                                         : ((const CONSTANT int32_t *)tokens)[t]);
-        }
+    for (int k = 0; k < TOK; ++k) {
+        const int64_t t = min(t0 + k, a.n_tokens - 1);   // past the end: the last one again
+        row[k] = row_of(a, a.index64 ? ((const CONSTANT int64_t *)tokens)[t] : ((const CONSTANT int32_t *)tokens)[t]);
+    }
 #pragma unroll
-        for (int k = 0; k < TOK; ++k)
-            if (row[k] >= 0) x[k] = load<TABLE, VEC>(table, row[k] * a.table_stride + c.col);
+    for (int k = 0; k < TOK; ++k)
+        if (row[k] >= 0) x[k] = load<TABLE, VEC>(table, row[k] * a.table_stride + c.col);
+    if (!c.on) return;
 #pragma unroll
-        for (int k = 0; k < TOK; ++k) {
-            if (!c.on || t0 + k >= a.n_tokens) break;
-            float v[VEC];
+    for (int k = 0; k < TOK; ++k) {
+        if (t0 + k >= a.n_tokens) break;
+        float v[VEC];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) v[j] = row[k] >= 0 ? __fmul_rn(a.scale, widen<TABLE>(x[k][j])) : 0.0f;
-            store<ACT, VEC>(out, (t0 + k) * a.act_stride + c.col, v, c.skip);
-        }
+        for (int j = 0; j < VEC; ++j) v[j] = row[k] >= 0 ? __fmul_rn(a.scale, widen<TABLE>(x[k][j])) : 0.0f;
+        store<ACT, VEC>(out, (t0 + k) * a.act_stride + c.col, v, c.skip);
     }
 }
 
@@ -265,6 +263,28 @@ __global__ void __launch_bounds__(kSortThreads) sort_tokens(EmbeddingArgs a, Emb
 }
 
 // ---------------------------------------------------------------- sum
+// Task z of writing zeros over a slab of a row without a position, from row
+// `from` on, when the whole gradient is written.
+template <int GRAD, int VEC>
+__device__ __forceinline__ void fill_row(const EmbeddingArgs &a, const EmbeddingWork &w, int slabs, int z, int64_t from,
+                                         void *grad)
+{
+    const CONSTANT int32_t *begin = (const CONSTANT int32_t *)w.begin;
+    const int64_t row = from + z / slabs;
+    if (row >= a.n_rows || (begin[row] != begin[row + 1] && row != w.pad_row)) return;
+    const Columns<VEC> c(z % slabs, int(threadIdx.x) % 64, a.width);
+    const float none[VEC] = {};
+    if (c.on) store<GRAD, VEC>(grad, row * a.grad_stride + c.col, none, c.skip);
+}
+
+template <int GRAD, int VEC>
+__global__ void __launch_bounds__(kWaves * 64)
+fill_rows(EmbeddingArgs a, EmbeddingWork w, int slabs, int tasks, int64_t from, void *grad)
+{
+    const int z = int(blockIdx.x) * kWaves + wave_of();
+    if (z < tasks) fill_row<GRAD, VEC>(a, w, slabs, z, from, grad);
+}
+
 // A wave keeps the rows and positions of its chunk and of as many entries
 // after it in its lanes (a chunk is at most 32 long), so that the addresses of
 // a batch are known without a load and all of a batch's loads, of dout and of
@@ -272,24 +292,16 @@ __global__ void __launch_bounds__(kSortThreads) sort_tokens(EmbeddingArgs a, Emb
 // STREAM: dout is read past the caches.
 template <int ACT, int GRAD, int VEC, bool ACC, bool STREAM>
 __global__ void __launch_bounds__(kWaves * 64)
-sum_runs(EmbeddingArgs a, EmbeddingWork w, int slabs, int tasks, int fill_rows, const void *dout, void *grad)
+sum_runs(EmbeddingArgs a, EmbeddingWork w, int slabs, int tasks, const void *dout, void *grad)
 {
     constexpr int AHEAD = 8;
     const int task = int(blockIdx.x) * kWaves + wave_of();
     const int lane = int(threadIdx.x) % 64;
     const CONSTANT int32_t *begin = (const CONSTANT int32_t *)w.begin;
     if (task >= tasks) {
-        // beyond the chunks: rows without a position, when the whole gradient
-        // is written
+        // beyond the chunks: rows without a position
         const int z = task - (tasks + kWaves - 1) / kWaves * kWaves;
-        if (ACC || z < 0 || z >= fill_rows * slabs) return;
-        const int first = z / slabs;
-        const Columns<VEC> c(z - first * slabs, lane, a.width);
-        const float none[VEC] = {};
-        for (int64_t row = first; row < a.n_rows; row += fill_rows) {
-            if (begin[row] != begin[row + 1] && row != w.pad_row) continue;
-            if (c.on) store<GRAD, VEC>(grad, row * a.grad_stride + c.col, none, c.skip);
-        }
+        if (!ACC && z >= 0) fill_row<GRAD, VEC>(a, w, slabs, z, 0, grad);
         return;
     }
     const int chunk = task / slabs;
@@ -472,21 +484,30 @@ __global__ void __launch_bounds__(kJoinWaves * 64) join_runs(EmbeddingArgs a, Em
 }
 
 template <int TABLE, int ACT, int VEC>
-hipError_t lookup_vec(const EmbeddingArgs &a, const void *table, const void *tokens, void *out, hipStream_t s)
+hipError_t lookup_vec(EmbeddingArgs a, const void *table, const void *tokens, void *out, hipStream_t s)
 {
-    const int64_t slabs = slabs_of<VEC>(a.width);
+    const int64_t slabs = slabs_of<VEC>(a.width), all = a.n_tokens;
     // four rows a wave once that leaves every CU sixteen waves
-    const bool four = a.n_tokens * slabs >= 4 * 256 * 16;
-    const int64_t groups = four ? (a.n_tokens + kLookupRows - 1) / kLookupRows : a.n_tokens;
-    // a launch has a limited number of workgroups: beyond kMostWaves each goes
-    // on to further rows
-    const int64_t tasks = std::min(groups, std::max<int64_t>(1, kMostWaves / slabs)) * slabs;
-    const dim3 g(static_cast<unsigned>((tasks + kLookupWaves - 1) / kLookupWaves)), b(kLookupWaves * 64);
-    if (four)
-        hipLaunchKernelGGL((lookup<TABLE, ACT, VEC, kLookupRows>), g, b, 0, s, a, int(slabs), table, tokens, out);
-    else
-        hipLaunchKernelGGL((lookup<TABLE, ACT, VEC, 1>), g, b, 0, s, a, int(slabs), table, tokens, out);
-    return hipGetLastError();
+    const bool four = all * slabs >= kLookupRows * 256 * 16;
+    const int64_t each = four ? kLookupRows : 1;
+    // a launch's grid is limited: kMostWaves of them, then the next launch
+    const int64_t most = std::max<int64_t>(1, kMostWaves / slabs) * each;
+    const char *tok = static_cast<const char *>(tokens);
+    char *dst = static_cast<char *>(out);
+    for (int64_t t = 0; t < all; t += most) {
+        a.n_tokens = std::min(most, all - t);
+        const int64_t tasks = (a.n_tokens + each - 1) / each * slabs;
+        const dim3 g(static_cast<unsigned>((tasks + kLookupWaves - 1) / kLookupWaves)), b(kLookupWaves * 64);
+        const void *from = tok + t * (a.index64 ? 8 : 4);
+        void *to = dst + t * a.act_stride * int64_t(sizeof(typename Raw<ACT, 1>::elem));
+        if (four)
+            hipLaunchKernelGGL((lookup<TABLE, ACT, VEC, kLookupRows>), g, b, 0, s, a, int(slabs), table, from, to);
+        else
+            hipLaunchKernelGGL((lookup<TABLE, ACT, VEC, 1>), g, b, 0, s, a, int(slabs), table, from, to);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 template <int TABLE, int ACT>
@@ -527,17 +548,29 @@ hipError_t sum_vec(const EmbeddingArgs &a, const void *dout, void *grad, bool ac
 {
     const int64_t slabs = slabs_of<VEC>(a.width);
     const int64_t tasks = w.n_chunks * slabs;
-    // rows that are filled at a time: a wave goes on to further ones
-    const int64_t fill_rows = accumulate ? 0 : std::min(a.n_rows, std::max<int64_t>(1, kMostWaves / slabs));
-    const int64_t blocks = (tasks + kWaves - 1) / kWaves + (fill_rows * slabs + kWaves - 1) / kWaves;
+    // the rows that are filled: by the same launch, or, as a launch's grid is
+    // limited, by further ones
+    const bool beside = !accumulate && a.n_rows * slabs <= kMostWaves;
+    if (!accumulate && !beside) {
+        const int64_t most = std::max<int64_t>(1, kMostWaves / slabs);
+        for (int64_t from = 0; from < a.n_rows; from += most) {
+            const int64_t z = std::min(most, a.n_rows - from) * slabs;
+            const dim3 g(static_cast<unsigned>((z + kWaves - 1) / kWaves)), b(kWaves * 64);
+            hipLaunchKernelGGL((fill_rows<GRAD, VEC>), g, b, 0, s, a, w, int(slabs), int(z), from, grad);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+    }
+    const int64_t fill = beside ? a.n_rows * slabs : 0;
+    const int64_t blocks = (tasks + kWaves - 1) / kWaves + (fill + kWaves - 1) / kWaves;
     if (blocks == 0) return hipSuccess;
     const dim3 g(static_cast<unsigned>(blocks)), b(kWaves * 64);
     if (accumulate)
-        hipLaunchKernelGGL((sum_runs<ACT, GRAD, VEC, true, STREAM>), g, b, 0, s, a, w, int(slabs), int(tasks),
-                           int(fill_rows), dout, grad);
+        hipLaunchKernelGGL((sum_runs<ACT, GRAD, VEC, true, STREAM>), g, b, 0, s, a, w, int(slabs), int(tasks), dout,
+                           grad);
     else
-        hipLaunchKernelGGL((sum_runs<ACT, GRAD, VEC, false, STREAM>), g, b, 0, s, a, w, int(slabs), int(tasks),
-                           int(fill_rows), dout, grad);
+        hipLaunchKernelGGL((sum_runs<ACT, GRAD, VEC, false, STREAM>), g, b, 0, s, a, w, int(slabs), int(tasks), dout,
+                           grad);
     return hipGetLastError();
 }
 

@@ -123,7 +123,8 @@ __device__ __forceinline__ int row_of(const EmbeddingArgs &a, int64_t tok)
     return r < uint64_t(a.n_rows) ? int(r) : -1;
 }
 
-// Waves of a launch that covers rows of any number, at most.
+// Waves of a launch that covers rows of any number, at most; further rows go to
+// the next launch.
 constexpr int64_t kMostWaves = int64_t(1) << 20;
 
 constexpr int kWaves = 4;   // of a workgroup of the row kernels

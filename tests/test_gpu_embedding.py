@@ -475,7 +475,7 @@ def test_padding_between_other_rows_of_a_chunk(V, lead):
 
 
 def test_more_rows_than_a_launch_has_waves():
-    """The lookup's and the filled rows' waves go on to further rows."""
+    """The lookup and the filled rows take further launches."""
     torch, ddp = _torch(), _lib()
     V, H, T = 1300003, 300, 4500001   # narrow rows: one wave a row, four rows a lookup's wave
     say("case waves", V, H, T)
