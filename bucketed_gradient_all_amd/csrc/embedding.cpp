@@ -43,6 +43,8 @@ int check_desc(const ddp_embedding_desc *d, int64_t n_tokens)
     if (!d) return fail(DDP_ERR_INVALID, "desc is NULL");
     if (d->n_rows < 0 || d->n_rows >= std::numeric_limits<int32_t>::max())
         return fail(DDP_ERR_INVALID, "n_rows must be in [0, 2^31 - 1)");
+    if (d->first_row > std::numeric_limits<int64_t>::max() - d->n_rows)
+        return fail(DDP_ERR_INVALID, "first_row + n_rows exceeds 2^63 - 1");
     if (d->width < 0 || d->width > std::numeric_limits<int32_t>::max())
         return fail(DDP_ERR_INVALID, "width must be in [0, 2^31)");
     if (d->index_dtype != DDP_I32 && d->index_dtype != DDP_I64)

@@ -561,7 +561,7 @@ enum {
 typedef struct {
     int64_t n_rows;         /* V, 0 <= V < 2^31 - 1                                                 */
     int64_t width;          /* H, 0 <= H < 2^31                                                     */
-    int64_t first_row;      /* index of row 0                                                       */
+    int64_t first_row;      /* index of row 0; first_row + V <= 2^63 - 1                             */
     int64_t padding_idx;    /* index whose positions contribute no gradient (it is looked up like
                                any other); a negative value: none                                   */
     int64_t table_stride;   /* elements from one row of the table to the next, >= H                 */

@@ -371,6 +371,33 @@ def test_the_list_of_a_reducer(W, collective):
     ddp.ddp_reducer_destroy(r)
 
 
+def test_the_list_of_a_static_reducer():
+    """Its tables lie in the library's own area; the list's are its own."""
+    torch, ddp = _torch(), _lib()
+    numel, W = [5000, 3], 3
+    plan = ddp.ddp_plan_buckets([4 * n for n in numel], ddp.DDP_ORDER_REVERSE, 1 << 30, 1 << 30)
+    flat = [torch.full((5003,), float(w + 1), device="cuda") for w in range(W)]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    desc = ddp.Desc(W, numel, plan.bucket_of, plan.offset_in_bucket, plan.n_buckets, ddp.DDP_IN_F32_VIEW,
+                    flat=[f.data_ptr() for f in flat], compute_stream=s.cuda_stream, comm_stream=s.cuda_stream)
+    r = ddp.ddp_reducer_create_static(desc)
+    g = ddp.make_reducer_grads(r)
+    ddp.ddp_prepare_for_backward(r)
+    ddp.ddp_mark_ready_many(r, [1, 0])
+    ddp.ddp_finish(r)
+    norm = new_norm()
+    torch.cuda.synchronize()
+    ddp.ddp_clip_grad_norm(g, ddp.DDP_NORM_INF, 1.0, norm.data_ptr(), s.cuda_stream)
+    torch.cuda.synchronize()
+    # 2 three times over thirds: each term one rounding, two additions
+    assert abs(float(norm) - 2.0) <= 2.0 * 5 * U32
+    # 2 * (1 / (2 + 1e-6)) is 5e-7 below 1, and 10 roundings
+    assert all(bool(((f - 1.0).abs() <= 5e-7 + 10 * U32).all()) for f in flat)
+    ddp.ddp_grads_destroy(g)
+    ddp.ddp_reducer_destroy(r)
+
+
 # ---------------------------------------------------------------- streams and graphs
 @pytest.mark.parametrize("size", [300, 500000])
 def test_replays_of_a_captured_clip(size):

@@ -114,6 +114,7 @@ def _desc(**kw):
 
 @pytest.mark.parametrize("kw,text", [
     ({"n_rows": -1}, "n_rows"), ({"n_rows": (1 << 31) - 1}, "n_rows"),
+    ({"first_row": (1 << 63) - 100}, "first_row"), ({"first_row": (1 << 63) - 1}, "first_row"),
     ({"width": -1}, "width"), ({"width": 1 << 31}, "width"),
     ({"index_dtype": 2}, "index type"), ({"table_dtype": 3}, "element type"), ({"grad_dtype": -1}, "element type"),
     ({"act_dtype": 9}, "element type"), ({"table_stride": 63}, "table_stride"), ({"grad_stride": 63}, "grad_stride"),
@@ -184,6 +185,26 @@ def test_embedding_workspace_serves_every_shorter_call(width, act):
     # about a quarter of the positions' rows of fp32 at most
     n = 1 << 20
     assert ddp.ddp_embedding_grad_workspace_bytes(d, n) <= n // 4 * 4 * (width + 3) + 8 * n + 4 * 101 + 8 * 256
+
+
+def test_the_header_is_c(tmp_path):
+    """A C program that names every new type and entry point compiles."""
+    if shutil.which("gcc") is None:
+        pytest.skip("needs gcc")
+    src = tmp_path / "use.c"
+    src.write_text("""#include "ddp.h"
+int use(void) {
+    ddp_grads_desc g = {0}; ddp_embedding_desc e = {0}; ddp_grads *l = 0; size_t n = 0; float norm = 0;
+    int rc = ddp_grads_create(&g, &l) + ddp_grads_from_reducer(0, 0, 0, &l) + ddp_grads_scratch_bytes(l, &n);
+    n += ddp_grads_workspace_bytes(&g) + ddp_reducer_grads_workspace_bytes(0);
+    rc += ddp_grad_norm(l, DDP_NORM_L2, &norm, 0, 0, 0) + ddp_clip_grad_norm(l, DDP_NORM_INF, 1.0f, &norm, 0, n, 0);
+    rc += ddp_clip_grads(l, 1.0f, &norm, 0) + ddp_grads_destroy(l);
+    n += ddp_embedding_grad_workspace_bytes(&e, 1);
+    return rc + ddp_embedding_lookup(&e, 0, 0, 0, 0, 0) + ddp_embedding_grad(&e, 0, 0, 0, 0, DDP_BF16, 0, n, 0);
+}
+""")
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-pedantic", "-I", os.path.join(ROOT, "include"), "-c", str(src),
+                    "-o", str(tmp_path / "use.o")], check=True, timeout=120)
 
 
 def test_host_sources_under_sanitizers(tmp_path):
