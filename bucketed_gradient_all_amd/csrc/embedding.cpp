@@ -115,8 +115,8 @@ int64_t slabs_of(const ddp_embedding_desc &d)
 
 // Positions of a chunk: as many as still leave kWantedWaves waves, 8 to 32.
 // Longer chunks cut fewer runs and leave the join less; the waves fill the chip
-// (32768 positions of 2048 columns: chunks of 32 56.2 us and the join 5.5, of
-// 16 53.8 and 7.6, of 8 56.0 and 12.6).
+// (32768 positions of 2048 columns: chunks of 32 55.3 us and the join 5.6, of
+// 16 53.1 and 9.8).
 int32_t chunk_of(const ddp_embedding_desc &d, int64_t n_tokens)
 {
     int32_t c = 8;
