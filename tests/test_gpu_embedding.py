@@ -542,3 +542,87 @@ def test_nan_in_places_that_do_not_count(T, V, act):
     c.row[(~named).cuda()] = math.nan
     c.lookup()
     c.check_lookup()
+
+
+def test_lookup_in_an_empty_table():
+    torch, ddp = _torch(), _lib()
+    out = torch.full((7, 33), 5.0, device="cuda")
+    tok = torch.arange(7, device="cuda")
+    d = ddp.EmbeddingDesc(0, 33)
+    ddp.ddp_embedding_lookup(d, 0, tok.data_ptr(), 7, out.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert not bool(out.any())
+
+
+@pytest.mark.parametrize("first", [-20, -(1 << 40), 1 << 40, (1 << 63) - 41])
+@pytest.mark.parametrize("T", [300, 9000])
+def test_shards_anywhere_in_64_bits(first, T):
+    """Tables whose rows stand for negative indices, or for the largest."""
+    say("case first", first, T)
+    torch = _torch()
+    g = torch.Generator().manual_seed(T)
+    c = Case(T, 40, 17, seed=T)
+    rows = torch.randint(-40, 80, (T,), generator=g).clamp(max=39 if first > 1 << 62 else 80)
+    c.host_tokens = rows + first
+    c.tokens.copy_(c.host_tokens)
+    c.first = c.desc.c.first_row = first
+    c.run_grad(True)
+    c.run_grad(False)
+    c.lookup()
+    c.check_lookup()
+
+
+@pytest.mark.parametrize("scale", [0.0, -1.5, 1e20])
+@pytest.mark.parametrize("T", [300, 9000])
+def test_scales(scale, T):
+    """The gradient leaves the table's rows scaled once, and the lookup scales them again: with the largest scale
+    that is 1e20 * 1e20 = 1e40, past 2^128 - 2^103 = 3.4e38, from where on float32 rounds to infinity. A product of two float32 has 48 bits and is exact in 64; rounded once it is the one right answer, so the
+    lookup is compared with it bit for bit instead of within a tolerance."""
+    torch = _torch()
+    say("case scales", scale, T)
+    c = Case(T, 40, 17, kind="falling", scale=scale, seed=T)
+    c.run_grad(True)
+    c.run_grad(False)
+    c.lookup()
+    assert bool((outside(c.act_buf, c.act) == 9.0).all())
+    held = (c.host_tokens >= 0) & (c.host_tokens < c.V)
+    want = torch.zeros(T, c.H, dtype=torch.float32)
+    want[held] = (c.row.cpu().double()[c.host_tokens[held]] * c.scale32).float()
+    assert torch.equal(c.act.cpu(), want)
+
+
+@pytest.mark.parametrize("T", [500, 9000])
+def test_strides_of_their_own(T):
+    """The table, the gradient and the positions' rows with three strides."""
+    torch, ddp = _torch(), _lib()
+    V, H = 60, 45
+    c = Case(T, V, H, kind="wild", seed=T)
+    c.act_buf, c.act = strided(T, H, 47, torch.float32, 1)
+    c.row_buf, c.row = strided(V, H, 64, torch.float32, 2)
+    c.desc = ddp.EmbeddingDesc(V, H, table_stride=64, grad_stride=64, act_stride=47)
+    c.run_grad(True)
+    c.run_grad(False)
+    c.lookup()
+    c.check_lookup()
+    grad_buf, grad = strided(V, H, 51, torch.bfloat16, 3)
+    d = ddp.EmbeddingDesc(V, H, table_dtype=0, grad_dtype=1, table_stride=64, grad_stride=51, act_stride=47)
+    n = ddp.ddp_embedding_grad_workspace_bytes(d, T)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    before = grad.cpu().clone()
+    ddp.ddp_embedding_grad(d, c.act.data_ptr(), c.tokens.data_ptr(), T, grad.data_ptr(), True, ws.data_ptr(), n, c.stream())
+    c.row_buf, c.row = grad_buf, grad
+    c.check_grad(before, True)
+
+
+def test_one_row_for_many_positions():
+    """act_stride 0 past the size of the single launch."""
+    torch, ddp = _torch(), _lib()
+    c = Case(9000, 20, 50, kind="falling", seed=6)
+    one = c.act[:1].clone()
+    c.act.copy_(one.expand(9000, 50))
+    before = c.row.cpu().clone()
+    d = ddp.EmbeddingDesc(20, 50, act_stride=0)
+    n = ddp.ddp_embedding_grad_workspace_bytes(d, 9000)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    ddp.ddp_embedding_grad(d, one.data_ptr(), c.tokens.data_ptr(), 9000, c.row.data_ptr(), True, ws.data_ptr(), n,
+                           c.stream())
+    c.check_grad(before, True)

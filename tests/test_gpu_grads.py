@@ -233,6 +233,28 @@ def test_a_norm_below_the_bound_leaves_the_list_untouched(size):
     assert torch.equal(d.out_views[0][0].cpu(), d.values[0])
 
 
+@pytest.mark.parametrize("size,copies", [(500, 8), (30000, 8), (100000, 5)])
+def test_many_copies_of_a_small_list(size, copies):
+    torch, ddp = _torch(), _lib()
+    say("case copies", size, copies)
+    c = Case([size, 7], [0, 1], copies=copies, seed=copies)
+    norm = new_norm()
+    ddp.ddp_clip_grad_norm(c.make(), 2, 0.3, norm.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    want = ref_norm(c.flat64(), 2)
+    check_norm(float(norm), want)
+    check_clip(c, want, 0.3)
+    c.guards_hold()
+
+
+def test_tensors_of_no_elements_may_have_no_address():
+    torch, ddp = _torch(), _lib()
+    x = torch.full((10,), 2.0, device="cuda")
+    g = ddp.make_grads([0, 10, 0], [[0, x.data_ptr(), 3]])
+    norm = new_norm()
+    ddp.ddp_grad_norm(g, 2, norm.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    check_norm(float(norm), 40.0 ** 0.5)
+
+
 def test_a_bound_of_zero_gives_zeros():
     torch, ddp = _torch(), _lib()
     c = Case([100, 90000], seed=2)
