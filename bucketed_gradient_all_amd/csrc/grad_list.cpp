@@ -100,16 +100,20 @@ size_t table_bytes(const ddp_grads_desc &d)
 
 struct Range {
     uintptr_t lo, hi;
-    int32_t what;   // tensor index, for the message
+    int32_t what;   // tensor index for the message, or -1: the workspace
 };
 
 int check_overlap(std::vector<Range> &v)
 {
     std::sort(v.begin(), v.end(), [](const Range &a, const Range &b) { return a.lo < b.lo; });
     for (size_t i = 1; i < v.size(); ++i)
-        if (v[i].lo < v[i - 1].hi)
+        if (v[i].lo < v[i - 1].hi) {
+            if (v[i].what < 0 || v[i - 1].what < 0)
+                return fail(DDP_ERR_INVALID, "the workspace and gradient " +
+                                                 std::to_string(std::max(v[i].what, v[i - 1].what)) + " overlap");
             return fail(DDP_ERR_INVALID, "gradients " + std::to_string(v[i - 1].what) + " and " +
                                              std::to_string(v[i].what) + " of the list overlap");
+        }
     return DDP_OK;
 }
 
@@ -126,7 +130,8 @@ int create(const ddp_grads_desc *d, ddp_grads **out)
                     "workspace missing, misaligned or smaller than " + std::to_string(need) + " bytes");
     std::vector<GradSeg> segs;
     std::vector<int32_t> tile_seg;
-    std::vector<Range> ranges;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(d->workspace);
+    std::vector<Range> ranges{{at, at + need, -1}};
     int32_t norm_tiles = 0;
     for (int32_t r = 0; r < R; ++r) {
         for (int32_t i = 0; i < N; ++i) {
@@ -216,6 +221,11 @@ int check_call(const ddp_grads *g, int32_t norm_type, const float *norm, const v
     if (!scratch || scratch_bytes < need || reinterpret_cast<uintptr_t>(scratch) % 8)
         return fail(DDP_ERR_INVALID,
                     "scratch missing, misaligned or smaller than " + std::to_string(need) + " bytes");
+    // the first workgroup of the clipping pass writes the norm while others
+    // still read the partials
+    const uintptr_t to = reinterpret_cast<uintptr_t>(norm), from = reinterpret_cast<uintptr_t>(scratch);
+    if (to + sizeof(float) > from && to < from + need)
+        return fail(DDP_ERR_INVALID, "norm lies inside the scratch");
     return check_device(g, s);
 }
 

@@ -486,7 +486,8 @@ size_t ddp_grads_workspace_bytes(const ddp_grads_desc *desc);
  * *out is set only on success.
  * Errors: DDP_ERR_INVALID: bad sizes, types or alignment; a tensor that
  * overlaps another (counted or scaled twice), or an `out` that overlaps any
- * tensor or another `out`; DDP_ERR_HIP; DDP_ERR_NOMEM. */
+ * tensor or another `out`, or a workspace that overlaps any of them;
+ * DDP_ERR_HIP; DDP_ERR_NOMEM. */
 int ddp_grads_create(const ddp_grads_desc *desc, ddp_grads **out);
 
 /* The list of a reducer's results, clipped in place: the flat buffers that
@@ -519,8 +520,8 @@ int ddp_grads_scratch_bytes(const ddp_grads *g, size_t *bytes);
  * norm must not lie inside a tensor of the list. May be recorded into a HIP
  * graph.
  * Errors: DDP_ERR_INVALID (unknown norm, NULL or misaligned pointers, scratch
- * missing or too small, another device current than the list's, a stream of
- * another device), DDP_ERR_HIP. */
+ * missing or too small, norm inside the scratch, another device current than
+ * the list's, a stream of another device), DDP_ERR_HIP. */
 int ddp_grad_norm(const ddp_grads *g, int32_t norm_type, float *norm, void *scratch, size_t scratch_bytes,
                   void *stream);
 
@@ -576,10 +577,11 @@ typedef struct {
 } ddp_embedding_desc;
 
 /* out[t] = R(scale * table[tokens[t] - first_row]) for t in [0, n_tokens),
- * n_tokens in [0, 2^30]; 0 for an index the table does not hold: the product in fp32, R one rounding to
- * act_dtype. All pointers are device memory at multiples of their element's
- * size; out must overlap neither table nor tokens. Elements of out between
- * the rows are left alone. May be recorded into a HIP graph.
+ * n_tokens in [0, 2^30]; 0 for an index the table does not hold. The product is
+ * in fp32, R one rounding to act_dtype. All pointers are device memory at
+ * multiples of their element's size; out must overlap neither table nor
+ * tokens. Elements of out between the rows are left alone. May be recorded
+ * into a HIP graph.
  * Errors: DDP_ERR_INVALID (bad desc, NULL or misaligned pointers, a stream of
  * another device than the current one), DDP_ERR_HIP. */
 int ddp_embedding_lookup(const ddp_embedding_desc *desc, const void *table, const void *tokens, int64_t n_tokens,
@@ -593,16 +595,17 @@ size_t ddp_embedding_grad_workspace_bytes(const ddp_embedding_desc *desc, int64_
 
 /* grad[v] (+)= scale * sum of dout[t] over the positions t whose token is row
  * v's: with accumulate != 0 the sum is added to what grad holds and rows
- * without a position are not touched; with accumulate == 0 grad's old contents are not read and rows without a position become 0. Sums
- * are fp32, rounded once to grad_dtype. The order of the additions depends on
- * the sizes and the tokens alone: the same call gives the same bits every time
- * (no floating-point atomics). dout is not read at positions that do not count.
+ * without a position are not touched; with accumulate == 0 grad's old contents
+ * are not read and rows without a position become 0. Sums are fp32, rounded
+ * once to grad_dtype. The order of the additions depends on the sizes and the
+ * tokens alone: the same call gives the same bits every time (no
+ * floating-point atomics). dout is not read at positions that do not count.
  * The positions are sorted by token first (stable), then each row's are summed
  * once, a frequent token's in pieces that are added in order. All pointers are
  * device memory at multiples of their element's size (workspace: 256 bytes);
- * grad must overlap no other argument. A workspace
- * serves one call at a time: calls that may run at once, replays of captured
- * ones included, need one each. May be recorded into a HIP graph.
+ * grad and the workspace must overlap no other argument. A workspace serves
+ * one call at a time: calls that may run at once, replays of captured ones
+ * included, need one each. May be recorded into a HIP graph.
  * Errors: as ddp_embedding_lookup; DDP_ERR_INVALID for a missing or too small
  * workspace. */
 int ddp_embedding_grad(const ddp_embedding_desc *desc, const void *dout, const void *tokens, int64_t n_tokens,

@@ -231,6 +231,12 @@ void lists()
         expect(ddp_grad_norm(g, 2, nullptr, sc.at, scratch, s) == DDP_ERR_INVALID, name + ": no norm");
         expect(ddp_grad_norm(g, 2, &norm, nullptr, scratch, s) == DDP_ERR_INVALID, name + ": no scratch");
         expect(ddp_grad_norm(g, 2, &norm, sc.at, scratch - 1, s) == DDP_ERR_INVALID, name + ": short scratch");
+        float *inside = reinterpret_cast<float *>(sc.at), *last = inside + scratch / 4 - 1;
+        for (float *bad : {inside, last}) {
+            expect(ddp_grad_norm(g, 2, bad, sc.at, scratch, s) == DDP_ERR_INVALID, name + ": norm in the scratch");
+            expect(ddp_clip_grad_norm(g, 2, 1.0f, bad, sc.at, scratch, s) == DDP_ERR_INVALID,
+                   name + ": norm in the scratch");
+        }
         for (float bad : {-1.0f, __builtin_inff(), __builtin_nanf("")}) {
             expect(ddp_clip_grad_norm(g, 2, bad, &norm, sc.at, scratch, s) == DDP_ERR_INVALID, name + ": bound");
             expect(ddp_clip_grads(g, bad, &norm, s) == DDP_ERR_INVALID, name + ": bound");

@@ -499,6 +499,30 @@ def test_list_refusals_on_the_device():
         ddp.ddp_grad_norm(g, 2, norm.data_ptr(), s)
 
 
+def test_a_norm_in_the_scratch_and_a_workspace_in_a_tensor_are_refused():
+    torch, ddp = _torch(), _lib()
+    c = Case([100000], seed=16)
+    g = c.make()
+    s = torch.cuda.current_stream().cuda_stream
+    need = ddp.ddp_grads_scratch_bytes(g)
+    scratch = torch.zeros(need + 8, dtype=torch.uint8, device="cuda")
+    p = scratch.data_ptr()
+    for inside in (p, p + need - 4):
+        for call in (lambda: ddp.ddp_grad_norm(g, 2, inside, s, p, need),
+                     lambda: ddp.ddp_clip_grad_norm(g, 2, 0.5, inside, s, p, need)):
+            with pytest.raises(ddp.DDPError) as e:
+                call()
+            assert e.value.code == ddp.DDP_ERR_INVALID and "inside the scratch" in e.value.msg
+    ddp.ddp_grad_norm(g, 2, p + need, s, p, need)   # right behind it
+    check_norm(float(scratch[need:need + 4].view(torch.float32)), ref_norm(c.flat64(), 2))
+    x = torch.full((1 << 16,), 3.0, device="cuda")
+    with pytest.raises(ddp.DDPError) as e:
+        ddp.ddp_grads_create(ddp.GradsDesc([1 << 16], [[x.data_ptr()]], workspace=x.data_ptr() + 1024,
+                                           workspace_bytes=4096))
+    assert e.value.code == ddp.DDP_ERR_INVALID and "the workspace and gradient 0 overlap" in e.value.msg
+    assert bool((x == 3.0).all())
+
+
 def test_a_handle_dropped_with_its_calls_queued_on_another_stream():
     """The memory of its tables is not handed out before they have run."""
     torch, ddp = _torch(), _lib()

@@ -67,6 +67,15 @@ def test_list_workspace_and_pointers_are_checked():
     _refused(lambda: _create([64], [[A]], out_ptrs=[[B + 2]]), "misaligned")
 
 
+def test_a_workspace_that_overlaps_a_tensor_is_refused():
+    """Its upload would overwrite the gradient."""
+    need = ddp.ddp_grads_workspace_bytes(ddp.GradsDesc([64], [[A]]))
+    for ws in (A, A + 240, A - need // 16 * 16 + 16):
+        _refused(lambda: _create([64], [[A]], ws=ws), "the workspace and gradient 0 overlap")
+    _refused(lambda: _create([64], [[A]], out_ptrs=[[B]], ws=B), "the workspace and gradient 0 overlap")
+    _refused(lambda: _create([64, 64], [[B, A]], ws=A), "the workspace and gradient 1 overlap")
+
+
 def test_list_tensors_that_overlap_are_refused():
     _refused(lambda: _create([64, 64], [[A, A]]), "overlap")
     _refused(lambda: _create([64, 64], [[A, A + 252]]), "overlap")
