@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import os
 import subprocess
+import threading
 import weakref
 from typing import Callable, List, NamedTuple, Optional, Sequence
 
@@ -616,25 +617,57 @@ def ddp_grads_workspace_bytes(desc: GradsDesc) -> int:
     return int(n)
 
 
-def _release_grads(holder: list, L) -> None:
+class _GradsMemory:
+    """The torch allocations of one list, the stream they were allocated on,
+    and whether calls were queued on any other."""
+    __slots__ = ("tensors", "home", "elsewhere")
+
+    def __init__(self):
+        self.tensors, self.home, self.elsewhere = [], 0, False
+
+
+# Memory of released lists that calls on other streams than its own may still
+# read. It waits here for the next list, whose making drains the device. The
+# streams themselves are not asked: they are the caller's, named by bare
+# handles, and may have been destroyed by now. (An allocator that is told of a
+# stream records an event on it when the memory is freed.)
+_parked: list = []
+_parked_lock = threading.Lock()
+
+
+def _free_parked() -> None:
+    import torch
+
+    with _parked_lock:   # finalizers append meanwhile
+        old = list(_parked)
+        for device in {t.device for t in old}:
+            torch.cuda.synchronize(device)
+        del _parked[:len(old)]
+
+
+def _release_grads(holder: list, L, memory: _GradsMemory) -> None:
     h, holder[0] = holder[0], None
     if h:
         L.ddp_grads_destroy(h)
+    if memory.elsewhere:
+        _parked.extend(memory.tensors)
+    memory.tensors = []
 
 
 class Grads:
-    """Handle of a ddp_grads, and the scratch its calls use by default. A graph
-    that recorded a call reads the handle's tables at every replay: keep the
-    handle as long."""
+    """Handle of a ddp_grads, and the scratch its calls use by default. It may
+    be dropped with calls still queued, on any stream; their stream may be gone
+    by then. A graph that recorded a call reads the handle's tables at every
+    replay: keep the handle as long."""
 
     def __init__(self, handle: int):
         self._holder = [handle]
         self._lib = lib()
-        self._finalizer = weakref.finalize(self, _release_grads, self._holder, self._lib)
-        self.workspace = None                 # device allocations that live as long as the handle
+        self._memory = _GradsMemory()         # device allocations that live as long as the handle
+        self._finalizer = weakref.finalize(self, _release_grads, self._holder, self._lib, self._memory)
+        self.workspace = None
         self.scratch = None
         self._scratch = (None, 0)
-        self._streams = None                  # streams those allocations know to be used on
 
     @property
     def handle(self):
@@ -646,30 +679,20 @@ class Grads:
 
     def own(self, workspace, scratch) -> None:
         """Keeps the torch allocations that hold the list's tables and its
-        scratch. The allocator learns of every stream they are used on, so that
-        memory of a handle dropped with calls still queued is not handed out
-        before these have run."""
+        scratch, made on the current stream."""
         import torch
 
         self.workspace, self.scratch = workspace, scratch
-        self._streams = {torch.cuda.current_stream(workspace.device).cuda_stream}
+        self._memory.tensors = [workspace, scratch]
+        self._memory.home = torch.cuda.current_stream(workspace.device).cuda_stream
         self.set_scratch(scratch.data_ptr(), scratch.numel())
 
     def used_on(self, stream: int) -> None:
-        if self._streams is None or stream in self._streams:
-            return
-        import torch
-
-        dev = self.workspace.device
-        # 1 names the null stream too; 2 is the calling thread's own stream,
-        # which the allocator does not take: a handle used on it has to live
-        # until its calls have run
-        if stream == 2:
-            return
-        s = torch.cuda.ExternalStream(stream, device=dev) if stream > 1 else torch.cuda.default_stream(dev)
-        self.workspace.record_stream(s)
-        self.scratch.record_stream(s)
-        self._streams.add(stream)
+        """Notes that a call goes to this stream. Memory used on its own
+        stream alone may be freed at once: the allocator hands it out again in
+        that stream's order. 1 names the null stream too."""
+        if (0 if stream == 1 else stream or 0) != self._memory.home:
+            self._memory.elsewhere = True
 
 
 def ddp_grads_create(desc: GradsDesc) -> Grads:
@@ -693,7 +716,7 @@ def ddp_grads_from_reducer(r: Reducer, workspace: int, workspace_bytes: int) -> 
 
 def ddp_grads_destroy(g: Grads) -> None:
     g._finalizer.detach()
-    _release_grads(g._holder, g._lib)
+    _release_grads(g._holder, g._lib, g._memory)
 
 
 def ddp_grads_scratch_bytes(g: Grads) -> int:
@@ -729,6 +752,7 @@ def _idle_workspace(nbytes: int):
     written by kernels queued there."""
     import torch
 
+    _free_parked()
     ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
     torch.cuda.current_stream().synchronize()
     return ws
