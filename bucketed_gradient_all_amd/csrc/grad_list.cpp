@@ -17,8 +17,28 @@ using ddp::guarded;
 using ddp::hip_fail;
 using ddp::kGradTile;
 
+namespace {
+
+// Addresses [lo, hi).
+struct Span {
+    uintptr_t lo, hi;
+};
+
+// Sorted and apart.
+using Spans = std::vector<Span>;
+
+bool meets(const Spans &v, uintptr_t lo, uintptr_t hi)
+{
+    const auto it = std::partition_point(v.begin(), v.end(), [lo](const Span &s) { return s.hi <= lo; });
+    return it != v.end() && it->lo < hi;
+}
+
+}  // namespace
+
 struct ddp_grads {
     GradTables tables{};
+    Spans held;      // the tables and the gradients
+    Spans written;   // what clipping writes: the gradients in place, or the other buffers
     int device = -1;
     int blocks = 1;        // workgroups of the norm's pass
     int clip_blocks = 1;   // workgroups of the clipping pass
@@ -101,6 +121,7 @@ size_t table_bytes(const ddp_grads_desc &d)
 struct Range {
     uintptr_t lo, hi;
     int32_t what;   // tensor index for the message, or -1: the workspace
+    bool out;       // another buffer that clipping writes
 };
 
 int check_overlap(std::vector<Range> &v)
@@ -117,6 +138,22 @@ int check_overlap(std::vector<Range> &v)
     return DDP_OK;
 }
 
+// Those of the sorted ranges that `of` picks; touching ones become one.
+template <class F>
+Spans spans_of(const std::vector<Range> &v, F of)
+{
+    Spans s;
+    for (const Range &r : v) {
+        if (!of(r)) continue;
+        if (!s.empty() && s.back().hi == r.lo)
+            s.back().hi = r.hi;
+        else
+            s.push_back({r.lo, r.hi});
+    }
+    s.shrink_to_fit();
+    return s;
+}
+
 int create(const ddp_grads_desc *d, ddp_grads **out)
 {
     if (!out) return fail(DDP_ERR_INVALID, "out is NULL");
@@ -131,7 +168,7 @@ int create(const ddp_grads_desc *d, ddp_grads **out)
     std::vector<GradSeg> segs;
     std::vector<int32_t> tile_seg;
     const uintptr_t at = reinterpret_cast<uintptr_t>(d->workspace);
-    std::vector<Range> ranges{{at, at + need, -1}};
+    std::vector<Range> ranges{{at, at + need, -1, false}};
     int32_t norm_tiles = 0;
     for (int32_t r = 0; r < R; ++r) {
         for (int32_t i = 0; i < N; ++i) {
@@ -149,8 +186,8 @@ int create(const ddp_grads_desc *d, ddp_grads **out)
             if (!src || !dst) return fail(DDP_ERR_INVALID, "gradient " + std::to_string(i) + " has a NULL pointer");
             if (src % isz || dst % osz)
                 return fail(DDP_ERR_INVALID, "gradient " + std::to_string(i) + " is misaligned for its type");
-            ranges.push_back({src, src + isz * uintptr_t(n), i});
-            if (d->out) ranges.push_back({dst, dst + osz * uintptr_t(n), i});
+            ranges.push_back({src, src + isz * uintptr_t(n), i, false});
+            if (d->out) ranges.push_back({dst, dst + osz * uintptr_t(n), i, true});
             s.shift = int16_t(dst % 256 / osz);
             s.tile0 = int32_t(tile_seg.size());
             const int64_t tiles = (n + s.shift + kGradTile - 1) / kGradTile;
@@ -163,6 +200,8 @@ int create(const ddp_grads_desc *d, ddp_grads **out)
     if (rc != DDP_OK) return rc;
 
     std::unique_ptr<ddp_grads> g(new ddp_grads());
+    g->held = spans_of(ranges, [](const Range &r) { return !r.out; });
+    g->written = spans_of(ranges, [d](const Range &r) { return r.what >= 0 && r.out == (d->out != nullptr); });
     hipError_t e = hipGetDevice(&g->device);
     int cus = 0;
     if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, g->device);
@@ -209,8 +248,17 @@ int check_device(const ddp_grads *g, hipStream_t s)
     return ddp::check_stream(s, now);
 }
 
+// What a call writes must lie apart from what it reads, of the other workgroups
+// too: partial sums over the tables would send them anywhere.
+int check_apart(const ddp_grads *g, const char *what, uintptr_t lo, size_t bytes, bool clips)
+{
+    if (meets(g->held, lo, lo + bytes) || (clips && meets(g->written, lo, lo + bytes)))
+        return fail(DDP_ERR_INVALID, std::string(what) + " overlaps a tensor or the workspace of the gradient list");
+    return DDP_OK;
+}
+
 int check_call(const ddp_grads *g, int32_t norm_type, const float *norm, const void *scratch, size_t scratch_bytes,
-               hipStream_t s)
+               bool clips, hipStream_t s)
 {
     if (!g) return fail(DDP_ERR_INVALID, "the gradient list is NULL");
     if (norm_type != DDP_NORM_INF && norm_type != DDP_NORM_L1 && norm_type != DDP_NORM_L2)
@@ -226,7 +274,9 @@ int check_call(const ddp_grads *g, int32_t norm_type, const float *norm, const v
     const uintptr_t to = reinterpret_cast<uintptr_t>(norm), from = reinterpret_cast<uintptr_t>(scratch);
     if (to + sizeof(float) > from && to < from + need)
         return fail(DDP_ERR_INVALID, "norm lies inside the scratch");
-    return check_device(g, s);
+    int rc = check_apart(g, "norm", to, sizeof(float), clips);
+    if (rc == DDP_OK) rc = check_apart(g, "scratch", from, need, clips);
+    return rc == DDP_OK ? check_device(g, s) : rc;
 }
 
 int check_max_norm(float max_norm)
@@ -358,7 +408,7 @@ int ddp_grad_norm(const ddp_grads *g, int32_t norm_type, float *norm, void *scra
 {
     return guarded([&] {
         const hipStream_t s = ddp::stream_of(stream);
-        const int rc = check_call(g, norm_type, norm, scratch, scratch_bytes, s);
+        const int rc = check_call(g, norm_type, norm, scratch, scratch_bytes, false, s);
         if (rc != DDP_OK) return rc;
         hipError_t e;
         if (g->tables.norm_tiles <= ddp::kSmallNorm) {
@@ -376,7 +426,7 @@ int ddp_clip_grad_norm(const ddp_grads *g, int32_t norm_type, float max_norm, fl
 {
     return guarded([&] {
         const hipStream_t s = ddp::stream_of(stream);
-        int rc = check_call(g, norm_type, norm, scratch, scratch_bytes, s);
+        int rc = check_call(g, norm_type, norm, scratch, scratch_bytes, true, s);
         if (rc == DDP_OK) rc = check_max_norm(max_norm);
         if (rc != DDP_OK) return rc;
         hipError_t e;
@@ -403,6 +453,10 @@ int ddp_clip_grads(const ddp_grads *g, float max_norm, const float *norm, void *
         if (!g) return fail(DDP_ERR_INVALID, "the gradient list is NULL");
         if (!norm || reinterpret_cast<uintptr_t>(norm) % 4)
             return fail(DDP_ERR_INVALID, "norm is NULL or misaligned");
+        // every workgroup reads it, while others write already
+        const uintptr_t at = reinterpret_cast<uintptr_t>(norm);
+        if (meets(g->written, at, at + sizeof(float)))
+            return fail(DDP_ERR_INVALID, "norm lies where the call writes");
         int rc = check_max_norm(max_norm);
         if (rc == DDP_OK) rc = check_device(g, s);
         if (rc != DDP_OK) return rc;

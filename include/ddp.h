@@ -517,11 +517,11 @@ int ddp_grads_scratch_bytes(const ddp_grads *g, size_t *bytes);
  * Sums run in 64 bits in a fixed order and are rounded to fp32 once: the same
  * list gives the same bits every time, and no square overflows. A NaN
  * anywhere gives NaN, otherwise an infinity inf; a list of no elements 0.
- * norm must not lie inside a tensor of the list. May be recorded into a HIP
- * graph.
+ * May be recorded into a HIP graph.
  * Errors: DDP_ERR_INVALID (unknown norm, NULL or misaligned pointers, scratch
- * missing or too small, norm inside the scratch, another device current than
- * the list's, a stream of another device), DDP_ERR_HIP. */
+ * missing or too small, norm inside the scratch, norm or scratch inside a
+ * tensor or the workspace of the list, another device current than the list's,
+ * a stream of another device), DDP_ERR_HIP. */
 int ddp_grad_norm(const ddp_grads *g, int32_t norm_type, float *norm, void *scratch, size_t scratch_bytes,
                   void *stream);
 
@@ -532,12 +532,14 @@ int ddp_grad_norm(const ddp_grads *g, int32_t norm_type, float *norm, void *scra
  * makes every result NaN, an infinite one makes finite gradients 0 and
  * infinite ones NaN: look at *norm before the optimizer's step. The norm is
  * written to *norm as it was before clipping.
- * Errors as ddp_grad_norm; DDP_ERR_INVALID unless 0 <= max_norm < inf. */
+ * Errors as ddp_grad_norm; DDP_ERR_INVALID unless 0 <= max_norm < inf, and if
+ * norm or scratch lie inside an `out`. */
 int ddp_clip_grad_norm(const ddp_grads *g, int32_t norm_type, float max_norm, float *norm, void *scratch,
                        size_t scratch_bytes, void *stream);
 
 /* The scaling alone, with a norm that is given (device, one float): e.g. of
- * several ranks' lists, summed. Errors as ddp_clip_grad_norm. */
+ * several ranks' lists, summed. Errors as ddp_clip_grad_norm, but norm may
+ * lie anywhere except where the call writes. */
 int ddp_clip_grads(const ddp_grads *g, float max_norm, const float *norm, void *stream);
 
 /* ---------------------------------------------------------------------------
