@@ -291,6 +291,7 @@ struct ReducerDesc {
     std::vector<int64_t> numel;
     std::vector<const void *> ptrs;
     ddp_grads_desc d{};
+    int device = -1;
 };
 
 int reducer_desc(const ddp_reducer *r, ReducerDesc &out)
@@ -298,6 +299,7 @@ int reducer_desc(const ddp_reducer *r, ReducerDesc &out)
     if (!r) return fail(DDP_ERR_INVALID, "reducer is NULL");
     const ddp::ReducerBuffers b = ddp::reducer_buffers(r);
     if (!b.flat) return fail(DDP_ERR_INVALID, "reducer has no device");
+    out.device = b.device;
     if (b.reduce_scatter) {
         for (int32_t k = 0; k < b.n_buckets; ++k) {
             const int64_t n = b.bucket_bytes[k] / 4;
@@ -382,6 +384,13 @@ int ddp_grads_from_reducer(const ddp_reducer *r, void *workspace, size_t workspa
         ReducerDesc d;
         const int rc = reducer_desc(r, d);
         if (rc != DDP_OK) return rc;
+        // the list will launch on the device that is current now
+        int now = -1;
+        const hipError_t e = hipGetDevice(&now);
+        if (e != hipSuccess) return hip_fail("current device", e);
+        if (now != d.device)
+            return fail(DDP_ERR_INVALID, "the reducer is on device " + std::to_string(d.device) +
+                                             ", the current device is " + std::to_string(now));
         d.d.workspace = workspace;
         d.d.workspace_bytes = workspace_bytes;
         return create(&d.d, out);

@@ -53,6 +53,7 @@ struct ReducerBuffers {
     const int64_t *bucket_bytes;   // [n_buckets]
     const int64_t *bucket_flat;    // [n_buckets] byte offset in the flat buffers
     float *const *flat;            // [world], or NULL for a reducer without a device
+    int device;
 };
 ReducerBuffers reducer_buffers(const ddp_reducer *r) noexcept;
 

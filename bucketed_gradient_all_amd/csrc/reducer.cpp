@@ -342,6 +342,7 @@ struct ddp_reducer {
     int static_device = -1;
     uint64_t static_generation = 0;
     std::vector<float *> flat;   // [W] the caller's flat buffers (empty without a device)
+    int ordinal = -1;            // the device that was current when it was created
     hipStream_t compute = nullptr, comm = nullptr;
     // ev_ready: compute -> comm before a launch; ev_done: comm -> compute at
     // finish (device-scope release suffices between two streams of one
@@ -989,6 +990,7 @@ int create_reducer(const ddp_reducer_desc *desc, ddp_reducer **out, bool static_
             if (e == hipSuccess) e = hipEventCreateWithFlags(&r->ev_foreign, hipEventDisableTiming);
         }
         if (e != hipSuccess) return hip_fail("reducer setup (device attributes, events, staging)", e);
+        r->ordinal = dev;
     }
     r->ready_order.reserve(size_t(pv.P));   // a backward's marks then allocate nothing
     r->set_groups(nullptr, 0);
@@ -1298,7 +1300,7 @@ namespace ddp {
 ReducerBuffers reducer_buffers(const ddp_reducer *r) noexcept
 {
     return {r->pv.W, r->pv.reduce_scatter, r->pv.B, r->pv.bucket_bytes.data(), r->pv.bucket_flat.data(),
-            r->device ? r->flat.data() : nullptr};
+            r->device ? r->flat.data() : nullptr, r->ordinal};
 }
 
 }  // namespace ddp

@@ -498,7 +498,8 @@ int ddp_grads_create(const ddp_grads_desc *desc, ddp_grads **out);
  * what their slices held (ddp_set_local_used), and count with it. Queue the
  * calls on the compute stream after ddp_finish. The list copies the pointers:
  * it may outlive the reducer.
- * Errors as ddp_grads_create; DDP_ERR_INVALID for a reducer without a device. */
+ * Errors as ddp_grads_create; DDP_ERR_INVALID for a reducer without a device,
+ * or with another device current than when the reducer was created. */
 size_t ddp_reducer_grads_workspace_bytes(const ddp_reducer *r);
 int ddp_grads_from_reducer(const ddp_reducer *r, void *workspace, size_t workspace_bytes, ddp_grads **out);
 

@@ -1,6 +1,7 @@
-"""Calls of the gradient lists that would write over what they read, on the
-CPU: the host sources under AddressSanitizer and UndefinedBehaviorSanitizer
-with stand-ins for the HIP runtime and the kernel launchers."""
+"""Gradient lists in unsafe places, on the CPU: calls that would write over what
+they read, and lists made on another device than their reducer's. The host
+sources run under AddressSanitizer and UndefinedBehaviorSanitizer with
+stand-ins for the HIP runtime and the kernel launchers."""
 import os
 import shutil
 import subprocess
@@ -34,3 +35,7 @@ def run_native(tmp_path, name, sources, extra=()):
 
 def test_a_norm_or_a_scratch_over_what_a_call_reads_is_refused(tmp_path):
     run_native(tmp_path, "list_alias_checks", ["reducer.cpp", "grad_list.cpp"])
+
+
+def test_the_list_of_a_reducer_is_made_on_its_device(tmp_path):
+    run_native(tmp_path, "list_device_checks", ["reducer.cpp", "grad_list.cpp"], ["-Wl,--wrap=hipGetDevice"])
