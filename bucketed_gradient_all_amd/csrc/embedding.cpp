@@ -224,6 +224,35 @@ int lookup(const ddp_embedding_desc *d, const void *table, const void *tokens, i
     return e == hipSuccess ? DDP_OK : hip_fail("embedding lookup", e);
 }
 
+// Whether one of n rows of `bytes` bytes, `stride` bytes apart, the first at p,
+// meets [lo, hi).
+bool rows_meet(const void *p, int64_t n, int64_t stride, int64_t bytes, uintptr_t lo, uintptr_t hi)
+{
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    uintptr_t first = 0;   // the first row that ends past lo
+    if (lo >= at + uintptr_t(bytes)) {
+        if (stride == 0) return false;
+        first = (lo - at - uintptr_t(bytes)) / uintptr_t(stride) + 1;
+    }
+    return first < uintptr_t(n) && at + first * uintptr_t(stride) < hi;
+}
+
+// The sum takes rows and positions from the workspace as they stand there:
+// written over, they would be addresses of anything.
+int check_workspace_apart(const ddp_embedding_desc &d, const void *dout, const void *tokens, int64_t n, const void *g,
+                          const void *workspace, size_t bytes)
+{
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(workspace), hi = lo + bytes;
+    const int64_t act = element_size(d.act_dtype), out = element_size(d.grad_dtype);
+    const int64_t index = d.index_dtype == DDP_I64 ? 8 : 4;
+    if (rows_meet(g, d.n_rows, d.grad_stride * out, d.width * out, lo, hi))
+        return fail(DDP_ERR_INVALID, "the workspace and grad overlap");
+    if (rows_meet(dout, n, d.act_stride * act, d.width * act, lo, hi))
+        return fail(DDP_ERR_INVALID, "the workspace and dout overlap");
+    if (rows_meet(tokens, n, index, index, lo, hi)) return fail(DDP_ERR_INVALID, "the workspace and tokens overlap");
+    return DDP_OK;
+}
+
 int grad(const ddp_embedding_desc *d, const void *dout, const void *tokens, int64_t n, void *g, bool accumulate,
          void *workspace, size_t workspace_bytes, hipStream_t s)
 {
@@ -254,7 +283,8 @@ int grad(const ddp_embedding_desc *d, const void *dout, const void *tokens, int6
     const int64_t wide = ceil_div(d->width, 64);   // slabs of the narrowest kernel, an upper bound
     if (wide > kMostSlabs || w.n_chunks * wide > kMostChunkWaves)
         return fail(DDP_ERR_INVALID, "n_tokens times width is too large for one call");
-    rc = check_device(s);
+    rc = check_workspace_apart(*d, dout, tokens, n, g, workspace, l.total);
+    if (rc == DDP_OK) rc = check_device(s);
     if (rc != DDP_OK) return rc;
     const EmbeddingArgs a = args_of(*d, n);
     ddp::SmallPlan small{};

@@ -610,7 +610,7 @@ size_t ddp_embedding_grad_workspace_bytes(const ddp_embedding_desc *desc, int64_
  * one call at a time: calls that may run at once, replays of captured ones
  * included, need one each. May be recorded into a HIP graph.
  * Errors: as ddp_embedding_lookup; DDP_ERR_INVALID for a missing or too small
- * workspace. */
+ * workspace, and for one that overlaps another argument. */
 int ddp_embedding_grad(const ddp_embedding_desc *desc, const void *dout, const void *tokens, int64_t n_tokens,
                        void *grad, int32_t accumulate, void *workspace, size_t workspace_bytes, void *stream);
 
