@@ -660,9 +660,9 @@ class Grads:
     by then. A graph that recorded a call reads the handle's tables at every
     replay: keep the handle as long."""
 
-    def __init__(self, handle: int):
+    def __init__(self, handle: int, L=None):
         self._holder = [handle]
-        self._lib = lib()
+        self._lib = L or lib()   # the library that created the list serves every call on it
         self._memory = _GradsMemory()         # device allocations that live as long as the handle
         self._finalizer = weakref.finalize(self, _release_grads, self._holder, self._lib, self._memory)
         self.workspace = None
@@ -711,7 +711,7 @@ def ddp_reducer_grads_workspace_bytes(r: Reducer) -> int:
 def ddp_grads_from_reducer(r: Reducer, workspace: int, workspace_bytes: int) -> Grads:
     h = ctypes.c_void_p()
     _check(r._lib.ddp_grads_from_reducer(r.handle, workspace or None, workspace_bytes, ctypes.byref(h)), r._lib)
-    return Grads(h.value)
+    return Grads(h.value, r._lib)
 
 
 def ddp_grads_destroy(g: Grads) -> None:

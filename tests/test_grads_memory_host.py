@@ -119,3 +119,28 @@ def test_a_failed_wait_frees_nothing(device, monkeypatch):
     with pytest.raises(RuntimeError):
         ddp._free_parked()
     assert ddp._parked == held
+
+
+def test_a_reducers_list_is_served_by_the_reducers_library(monkeypatch):
+    """Another library loaded since knows nothing of the list."""
+    calls = []
+
+    class Library:
+        def __init__(self, name):
+            self.name = name
+
+        def __getattr__(self, fn):
+            def call(*a):
+                calls.append((self.name, fn))
+                if fn == "ddp_grads_from_reducer":
+                    a[3]._obj.value = 0x1234
+                return 0
+            return call
+
+    old, new = Library("old"), Library("new")
+    monkeypatch.setattr(ddp, "_lib", new)
+    g = ddp.ddp_grads_from_reducer(types.SimpleNamespace(handle=1, _lib=old), 0x100, 64)
+    ddp.ddp_clip_grads(g, 1.0, 0x200, 0)
+    del g
+    gc.collect()
+    assert calls == [("old", "ddp_grads_from_reducer"), ("old", "ddp_clip_grads"), ("old", "ddp_grads_destroy")]
