@@ -18,9 +18,10 @@
 //   * Every order is fixed: a thread's elements, the threads of a wave, the
 //     waves of a workgroup, the workgroups' partials. No atomics; a list gives
 //     the same bits every time.
-//   * The workgroups of the clipping pass each reduce the partials for
-//     themselves (at most 16 KiB from L2) instead of waiting for a launch that
-//     does it once.
+//   * Lists of many tiles that go into other buffers finish the norm in a
+//     launch of its own. Otherwise the workgroups of the clipping pass, at most
+//     eight a CU, each reduce the partials for themselves (at most 8 KiB from
+//     L2) instead of waiting for such a launch.
 #include "../../include/ddp.h"
 #include "grad_list.h"
 

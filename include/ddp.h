@@ -441,7 +441,7 @@ int ddp_get_timings(const ddp_reducer *r, int32_t *first_bucket, int32_t *n_buck
  * What a training step does between the reduction and the optimizer: take the
  * norm over every gradient of the model, and scale all of them by
  * min(1, max_norm / (norm + 1e-6)). A list names the tensors once; the calls
- * on it then cost one or two launches however many tensors it holds.
+ * on it then cost one to three launches however many tensors it holds.
  * ------------------------------------------------------------------------- */
 enum {
     DDP_F32 = 0,
@@ -508,7 +508,7 @@ int ddp_grads_from_reducer(const ddp_reducer *r, void *workspace, size_t workspa
 int ddp_grads_destroy(ddp_grads *g);
 
 /* Device scratch that one call of ddp_grad_norm or ddp_clip_grad_norm needs
- * (at most 16 KiB, at least 8 bytes). Its contents mean nothing between calls.
+ * (at most 8 KiB, at least 8 bytes). Its contents mean nothing between calls.
  * A list is only read by the calls on it: any number of them may run at once,
  * on any streams and from replayed graphs, as long as each has a scratch of
  * its own (and no two scale the same tensors). */
