@@ -100,7 +100,11 @@ int check_device(hipStream_t s)
 constexpr int64_t kWantedWaves = 8192;
 
 // Bytes of dout from which it is read past the caches: well below the 256 MiB
-// of the last cache it may still lie there from the kernel that wrote it.
+// of the last cache it may still lie there from the kernel that wrote it. 2048
+// bf16 columns added to fp32, past the caches against through them: 32 MiB 34.6
+// us against 32.8, 64 MiB 49.2 against 48.8, 128 MiB 72.8 against 77.3, 256 MiB
+// 116 against 135; with dout written right before (that copy's time taken off),
+// 64 MiB 49.4 against 48.1, 128 MiB 72 against 74, 256 MiB 122 against 132.
 constexpr int64_t kStreamBytes = int64_t(64) << 20;
 
 // Waves side by side over a row's columns, and of the sum in all, at most:

@@ -18,7 +18,9 @@
 //          workgroups share nothing: where a range begins is the number of
 //          tokens of lower rows, which each workgroup counts as it goes. Tokens
 //          are few bytes beside dout and come from L2 after the first read.
-//   sum    56 us, 290 MB (5.2 TB/s), bound by memory. A wave takes a chunk of the
+//   sum    56 us, 290 MB at 5.2 TB/s, where plain streams reach 6.5; what holds
+//          it below has not been told apart (lanes load 8 bytes of dout, and the
+//          waves start behind three dependent loads). A wave takes a chunk of the
 //          sorted positions and a slab of columns and adds up run after run (the
 //          positions of one row). A run of at most a chunk's length belongs to
 //          the chunk it begins in, which goes beyond its end for it; only longer

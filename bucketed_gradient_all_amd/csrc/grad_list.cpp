@@ -223,14 +223,18 @@ int create(const ddp_grads_desc *d, ddp_grads **out)
     g->small = g->tables.all_tiles <= ddp::kSmallClip;
     // workgroups that go from tile to tile, as many as fill the chip. The norm
     // does best with four a CU (953M bf16 elements 285 us, eight 294, two 292)
-    // and leaves as many partials; clipping has stores too and takes eight.
+    // and leaves as many partials. Clipping takes eight: of two, four, eight,
+    // sixteen and thirty-two 335M fp32 elements in place take 476, 499, 496,
+    // 490 and 486 us to scale, 203 to 213 with the norm if they lie below the
+    // bound, and 30M into another buffer 61 to 63.
     g->blocks = std::max(1, std::min({norm_tiles, ddp::kMaxPartials, 4 * cus}));
     g->clip_blocks = std::max(1, std::min(g->tables.all_tiles, 8 * cus));
     // Into other buffers every tensor is written, so a workgroup a part of a
     // tile pays. In place there is mostly nothing to do but to see that the
-    // norm is below the bound, which 2048 workgroups do in 7 us; 41116, one a
-    // tile, took 11. Where they do scale, 335M fp32 elements on eight replicas
-    // take 3.50 ms (6.1 TB/s), as they do a workgroup a part.
+    // norm is below the bound, which 2048 workgroups do in 5 us; 41116, one a
+    // tile, took 11. The price: where they do scale, 335M fp32 elements on
+    // eight replicas take 4.14 ms (5.2 TB/s) against 3.58 (6.0 TB/s) with a
+    // workgroup a part.
     g->parts = !g->tables.in_place && g->tables.all_tiles > ddp::kManyTiles && g->tables.all_tiles <= kMostPartTiles;
     *out = g.release();
     return DDP_OK;

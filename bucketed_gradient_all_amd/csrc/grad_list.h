@@ -25,7 +25,11 @@ constexpr int kMaxPartials = 1024;
 
 // Lists of more than this many tiles that are clipped into other buffers are
 // clipped by a workgroup a part of a tile, with the norm finished by a launch
-// of its own before.
+// of its own before. That launch takes 4 to 5 us, the parts are a few percent
+// faster: replayed from a graph, fp32 into fp32, 2048 tiles 38.6 us against
+// 37.9 with workgroups that go from tile to tile, 4096 70.3 against 69.3, 8192
+// 133 against 136, 65536 1056 against 1126; bf16 into fp32, 1024 18.2 against
+// 18.1, 4096 49.1 against 50.2, 65536 691 against 752.
 constexpr int kManyTiles = 4096;
 
 // One tensor of a list. Its tiles are cut at absolute destination addresses
