@@ -261,8 +261,9 @@ __device__ __forceinline__ void clip_tile(const GradSeg &s, int64_t base, int ti
 __device__ __forceinline__ GradSeg seg_of(const GradTables &t, int tile)
 {
     typedef uint32_t words __attribute__((ext_vector_type(8)));
+    typedef words any __attribute__((aligned(16)));   // as the workspace is
     const int k = ((const CONSTANT int32_t *)t.tile_seg)[tile];
-    const words w = ((const CONSTANT words *)t.segs)[k];
+    const words w = ((const CONSTANT any *)t.segs)[k];
     return __builtin_bit_cast(GradSeg, w);
 }
 
