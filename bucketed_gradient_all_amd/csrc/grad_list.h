@@ -14,9 +14,10 @@ constexpr int kGradTile = 8192;
 
 // Lists of up to this many tiles are handled by one workgroup in one launch:
 // the norm, and the norm with clipping. Replayed from a graph, one launch
-// against two, with full tiles: the norm of 4 3.3 us against 4.7, of 12 5.4 against 4.9;
-// clipping of 4 tiles into another buffer 5.8 against 5.6, of 12 12.3 against
-// 5.7. Called one by one, the second launch costs the host about 3 us more.
+// against two, the tiles full: the norm of 4 tiles 3.3 us against 4.7, of 12
+// 5.4 against 4.9; clipping of 4 tiles into another buffer 5.8 against 5.6, of
+// 12 12.3 against 5.7. Called one by one, the second launch costs the host
+// about 3 us more.
 constexpr int kSmallNorm = 12, kSmallClip = 6;
 
 // Most workgroups the norm's pass is split over: each leaves one 8-byte
