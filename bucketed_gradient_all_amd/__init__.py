@@ -1,6 +1,6 @@
 """Python binding of libddp.so (include/ddp.h): bucketed gradient reduction
 for data-parallel training on MI355X (gfx950), the norm and clipping of the
-gradients, and the embedding's lookup and gradient.
+gradients, the AdamW step, and the embedding's lookup and gradient.
 
 Argument marshalling only: every step of the path runs in the C++ host
 library and its HIP kernels. The functions keep the C names; a negative
@@ -56,6 +56,10 @@ DDP_NORM_INF = 0
 DDP_NORM_L1 = 1
 DDP_NORM_L2 = 2
 
+DDP_STATE_F32 = 0
+DDP_STATE_8BIT = 1
+DDP_STATE_BLOCK = 128
+
 DDP_I32 = 0
 DDP_I64 = 1
 
@@ -64,11 +68,11 @@ HIPCC_FLAGS = ["--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17",
                "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 
 # one object per source; the kernel families compile in parallel
-SOURCES = ["reducer.cpp", "grad_list.cpp", "embedding.cpp", "bucket_reduce.hip", "bucket_bf16_hook.hip",
+SOURCES = ["reducer.cpp", "grad_list.cpp", "embedding.cpp", "adamw.cpp", "bucket_reduce.hip", "bucket_bf16_hook.hip",
            "bucket_fp16_hook.hip", "static_tables.hip", "grad_norm.hip", "embedding.hip",
-           "embedding_small.hip"]
+           "embedding_small.hip", "adamw.hip"]
 HEADERS = ["host_common.h", "internal.h", "reduce_kernels.h", "static_area.h", "grad_list.h", "embedding.h",
-           "embedding_kernels.h"]
+           "embedding_kernels.h", "element.h", "spans.h", "adamw.h"]
 
 
 BUILD_DIR = os.path.join(HERE, "_build")
@@ -156,6 +160,42 @@ class ddp_grads_desc(ctypes.Structure):
     ]
 
 
+class ddp_adamw_desc(ctypes.Structure):
+    _fields_ = [
+        ("n_tensors", ctypes.c_int32),
+        ("state", ctypes.c_int32),
+        ("numel", ctypes.c_void_p),
+        ("grad_dtype", ctypes.c_void_p),
+        ("param_dtype", ctypes.c_void_p),
+        ("grads", ctypes.c_void_p),
+        ("params", ctypes.c_void_p),
+        ("copies", ctypes.c_void_p),
+        ("copy_dtype", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("m_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("weight_decay", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class ddp_adamw_args(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("step", ctypes.c_int64),
+        ("lr_ptr", ctypes.c_void_p),
+        ("step_ptr", ctypes.c_void_p),
+        ("norm", ctypes.c_void_p),
+        ("max_norm", ctypes.c_float),
+        ("skip_nonfinite", ctypes.c_int32),
+    ]
+
+
 class ddp_embedding_desc(ctypes.Structure):
     _fields_ = [
         ("n_rows", ctypes.c_int64),
@@ -214,6 +254,9 @@ def lib():
             "ddp_grad_norm": [P, I32, P, P, SIZE, P],
             "ddp_clip_grad_norm": [P, I32, F32, P, P, SIZE, P],
             "ddp_clip_grads": [P, F32, P, P],
+            "ddp_adamw_create": [ctypes.POINTER(ddp_adamw_desc), ctypes.POINTER(ctypes.c_void_p)],
+            "ddp_adamw_destroy": [P],
+            "ddp_adamw_step": [P, ctypes.POINTER(ddp_adamw_args), P],
             "ddp_embedding_lookup": [ctypes.POINTER(ddp_embedding_desc), P, P, I64, P, P],
             "ddp_embedding_grad": [ctypes.POINTER(ddp_embedding_desc), P, P, I64, P, I32, P, SIZE, P],
         }
@@ -224,6 +267,7 @@ def lib():
         for name, args in {"ddp_workspace_bytes": [ctypes.POINTER(ddp_reducer_desc)],
                            "ddp_grads_workspace_bytes": [ctypes.POINTER(ddp_grads_desc)],
                            "ddp_reducer_grads_workspace_bytes": [P],
+                           "ddp_adamw_workspace_bytes": [ctypes.POINTER(ddp_adamw_desc)],
                            "ddp_embedding_grad_workspace_bytes": [ctypes.POINTER(ddp_embedding_desc), I64]}.items():
             f = getattr(L, name)
             f.argtypes = args
@@ -617,7 +661,7 @@ def ddp_grads_workspace_bytes(desc: GradsDesc) -> int:
     return int(n)
 
 
-class _GradsMemory:
+class _ListMemory:
     """The torch allocations of one list, the stream they were allocated on,
     and whether calls were queued on any other."""
     __slots__ = ("tensors", "home", "elsewhere")
@@ -645,47 +689,43 @@ def _free_parked() -> None:
         del _parked[:len(old)]
 
 
-def _release_grads(holder: list, L, memory: _GradsMemory) -> None:
+def _release_list(holder: list, destroy, memory: _ListMemory) -> None:
     h, holder[0] = holder[0], None
     if h:
-        L.ddp_grads_destroy(h)
+        destroy(h)
     if memory.elsewhere:
         _parked.extend(memory.tensors)
     memory.tensors = []
 
 
-class Grads:
-    """Handle of a ddp_grads, and the scratch its calls use by default. It may
-    be dropped with calls still queued, on any stream; their stream may be gone
-    by then. A graph that recorded a call reads the handle's tables at every
-    replay: keep the handle as long."""
+class _List:
+    """Handle of a native list of tensors. It may be dropped with calls still
+    queued, on any stream; their stream may be gone by then. A graph that
+    recorded a call reads the handle's tables at every replay: keep the handle
+    as long."""
+
+    _destroy = ""   # name of the library's call that releases the handle
 
     def __init__(self, handle: int, L=None):
         self._holder = [handle]
         self._lib = L or lib()   # the library that created the list serves every call on it
-        self._memory = _GradsMemory()         # device allocations that live as long as the handle
-        self._finalizer = weakref.finalize(self, _release_grads, self._holder, self._lib, self._memory)
+        self._memory = _ListMemory()          # device allocations that live as long as the handle
+        self._finalizer = weakref.finalize(self, _release_list, self._holder, getattr(self._lib, self._destroy),
+                                           self._memory)
         self.workspace = None
-        self.scratch = None
-        self._scratch = (None, 0)
 
     @property
     def handle(self):
         return self._holder[0]
 
-    def set_scratch(self, ptr: int, nbytes: int) -> None:
-        """The scratch of calls that are given none."""
-        self._scratch = (ptr or None, nbytes)
-
-    def own(self, workspace, scratch) -> None:
-        """Keeps the torch allocations that hold the list's tables and its
-        scratch, made on the current stream."""
+    def own(self, *tensors) -> None:
+        """Keeps the torch allocations that the list's calls use, the first of
+        them its tables, made on the current stream."""
         import torch
 
-        self.workspace, self.scratch = workspace, scratch
-        self._memory.tensors = [workspace, scratch]
-        self._memory.home = torch.cuda.current_stream(workspace.device).cuda_stream
-        self.set_scratch(scratch.data_ptr(), scratch.numel())
+        self.workspace = tensors[0]
+        self._memory.tensors = list(tensors)
+        self._memory.home = torch.cuda.current_stream(self.workspace.device).cuda_stream
 
     def used_on(self, stream: int) -> None:
         """Notes that a call goes to this stream. Memory used on its own
@@ -693,6 +733,29 @@ class Grads:
         that stream's order. 1 names the null stream too."""
         if (0 if stream == 1 else stream or 0) != self._memory.home:
             self._memory.elsewhere = True
+
+    def destroy(self) -> None:
+        self._finalizer()
+
+
+class Grads(_List):
+    """Handle of a ddp_grads, and the scratch its calls use by default."""
+
+    _destroy = "ddp_grads_destroy"
+
+    def __init__(self, handle: int, L=None):
+        super().__init__(handle, L)
+        self.scratch = None
+        self._scratch = (None, 0)
+
+    def set_scratch(self, ptr: int, nbytes: int) -> None:
+        """The scratch of calls that are given none."""
+        self._scratch = (ptr or None, nbytes)
+
+    def own(self, workspace, scratch) -> None:
+        super().own(workspace, scratch)
+        self.scratch = scratch
+        self.set_scratch(scratch.data_ptr(), scratch.numel())
 
 
 def ddp_grads_create(desc: GradsDesc) -> Grads:
@@ -715,8 +778,7 @@ def ddp_grads_from_reducer(r: Reducer, workspace: int, workspace_bytes: int) -> 
 
 
 def ddp_grads_destroy(g: Grads) -> None:
-    g._finalizer.detach()
-    _release_grads(g._holder, g._lib, g._memory)
+    g.destroy()
 
 
 def ddp_grads_scratch_bytes(g: Grads) -> int:
@@ -781,6 +843,101 @@ def make_reducer_grads(r: Reducer) -> Grads:
     nbytes = ddp_reducer_grads_workspace_bytes(r)
     ws = _idle_workspace(nbytes)
     return _with_scratch(ddp_grads_from_reducer(r, ws.data_ptr(), nbytes), ws)
+
+
+class AdamWDesc:
+    """Owns the host arrays a ddp_adamw_desc points to. Pointers, types and
+    decays per tensor; weight_decay may be one number for all; copy_ptrs may
+    hold 0 for tensors without a copy."""
+
+    def __init__(self, numel: Sequence[int], grad_ptrs: Sequence[int], param_ptrs: Sequence[int],
+                 m_ptrs: Sequence[int], v_ptrs: Sequence[int], grad_dtype: Optional[Sequence[int]] = None,
+                 param_dtype: Optional[Sequence[int]] = None, copy_ptrs: Optional[Sequence[int]] = None,
+                 copy_dtype: Optional[Sequence[int]] = None, state: int = DDP_STATE_F32,
+                 m_scale_ptrs: Optional[Sequence[int]] = None, v_scale_ptrs: Optional[Sequence[int]] = None,
+                 weight_decay=None, workspace: int = 0, workspace_bytes: int = 0):
+        self.numel = np.ascontiguousarray(numel, dtype=np.int64).reshape(-1)
+        N = self.numel.size
+        self.arrays = []   # keeps what the desc points to
+
+        def of(what, v, dtype):
+            if v is None:
+                return None
+            a = np.ascontiguousarray(v, dtype=dtype).reshape(-1)
+            if a.size != N:
+                raise ValueError(f"{what} needs {N} entries, got {a.size}")
+            self.arrays.append(a)
+            return a.ctypes.data
+
+        if weight_decay is not None and np.ndim(weight_decay) == 0:
+            weight_decay = np.full(N, weight_decay, np.float64)
+        d = ddp_adamw_desc()
+        d.n_tensors, d.state = N, state
+        d.numel = self.numel.ctypes.data
+        d.grad_dtype = of("grad_dtype", grad_dtype, np.int32)
+        d.param_dtype = of("param_dtype", param_dtype, np.int32)
+        d.grads = of("grad_ptrs", grad_ptrs, np.uint64)
+        d.params = of("param_ptrs", param_ptrs, np.uint64)
+        d.copies = of("copy_ptrs", copy_ptrs, np.uint64)
+        d.copy_dtype = of("copy_dtype", copy_dtype, np.int32)
+        d.m = of("m_ptrs", m_ptrs, np.uint64)
+        d.v = of("v_ptrs", v_ptrs, np.uint64)
+        d.m_scale = of("m_scale_ptrs", m_scale_ptrs, np.uint64)
+        d.v_scale = of("v_scale_ptrs", v_scale_ptrs, np.uint64)
+        d.weight_decay = of("weight_decay", weight_decay, np.float64)
+        d.workspace, d.workspace_bytes = workspace or None, workspace_bytes
+        self.c = d
+
+    def set_workspace(self, ptr: int, nbytes: int) -> None:
+        self.c.workspace = ptr or None
+        self.c.workspace_bytes = nbytes
+
+
+class AdamW(_List):
+    """Handle of a ddp_adamw."""
+
+    _destroy = "ddp_adamw_destroy"
+
+
+def ddp_adamw_workspace_bytes(desc: AdamWDesc) -> int:
+    n = lib().ddp_adamw_workspace_bytes(ctypes.byref(desc.c))
+    if n == 0:
+        raise DDPError(DDP_ERR_INVALID, ddp_last_error())
+    return int(n)
+
+
+def ddp_adamw_create(desc: AdamWDesc) -> AdamW:
+    h = ctypes.c_void_p()
+    _check(lib().ddp_adamw_create(ctypes.byref(desc.c), ctypes.byref(h)))
+    return AdamW(h.value)
+
+
+def ddp_adamw_destroy(o: AdamW) -> None:
+    o.destroy()
+
+
+def ddp_adamw_step(o: AdamW, lr: float, step: int, stream: int, beta1: float = 0.9, beta2: float = 0.999,
+                   eps: float = 1e-8, max_norm: float = 0.0, norm: int = 0, skip_nonfinite: bool = False,
+                   lr_ptr: int = 0, step_ptr: int = 0) -> None:
+    """norm, lr_ptr and step_ptr: device pointers (float, float, int64); with
+    the last two lr and step are not read."""
+    a = ddp_adamw_args(lr, beta1, beta2, eps, step, lr_ptr or None, step_ptr or None, norm or None, max_norm,
+                       1 if skip_nonfinite else 0)
+    o.used_on(stream)
+    _check(o._lib.ddp_adamw_step(o.handle, ctypes.byref(a), stream or None), o._lib)
+
+
+def make_adamw(numel: Sequence[int], grad_ptrs: Sequence[int], param_ptrs: Sequence[int], m_ptrs: Sequence[int],
+               v_ptrs: Sequence[int], **kw) -> AdamW:
+    """Creates an AdamW list on the current device from AdamWDesc's arguments;
+    its workspace is a torch allocation that the returned handle keeps alive."""
+    desc = AdamWDesc(numel, grad_ptrs, param_ptrs, m_ptrs, v_ptrs, **kw)
+    nbytes = ddp_adamw_workspace_bytes(desc)
+    ws = _idle_workspace(nbytes)
+    desc.set_workspace(ws.data_ptr(), nbytes)
+    o = ddp_adamw_create(desc)
+    o.own(ws)
+    return o
 
 
 class EmbeddingDesc:

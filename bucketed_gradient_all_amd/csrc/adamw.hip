@@ -1,0 +1,361 @@
+// One AdamW step over a list of tensors.
+//
+//   g = grad * f,  f = min(1, max_norm / (norm + 1e-6)), or 1 without a norm
+//   m = beta1 * m + (1 - beta1) * g
+//   v = beta2 * v + (1 - beta2) * g^2
+//   p = p * (1 - lr * decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+//   copy = R(p)                                  R: one rounding to the copy's type
+//
+// One pass over memory and no operand used twice, so it is bound by memory.
+// Everything is fp32 and every operation is rounded by itself (no product is
+// fused with a sum), with correctly rounded divisions and roots: about fifty
+// instructions an element, which the memory's time hides.
+//
+// 8-bit states: the m and r = sqrt(v) of a block of 128 elements are held as
+// e4m3 codes of m * (448 / max|m|), with max|m| / 448 as the block's scale.
+//   * The root, because the codes' range of 2^-9 to 448 then spans 2^35 of v, and
+//     because the root is what the step divides by.
+//   * A positive r never gets the code of zero: with r = 0 beside an m that is
+//     not, a later step with a small gradient would divide by eps alone. A root
+//     that is held too large only makes that element's step smaller.
+//   * The step itself uses this step's m and v before they are rounded.
+//   * The maximum is taken on the bit patterns as unsigned integers, where an
+//     infinity and a NaN are above every number: the scale is then not finite
+//     either, and no state of the block is.
+#include "../../include/ddp.h"
+#include "adamw.h"
+#include "element.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+namespace ddp {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVec = 4;
+constexpr int kGroups = kAdamTile / (kThreads * kVec);
+
+template <int TYPE>
+using Vec = typename Raw<TYPE, kVec>::type;
+
+// Those of four elements that the tensor has.
+struct Some {
+    int lo, hi;
+    __device__ __forceinline__ bool all() const { return lo == 0 && hi == kVec; }
+};
+
+template <bool FULL>
+__device__ __forceinline__ Some some_of(int64_t e, int64_t len)
+{
+    if (FULL) return {0, kVec};
+    return {int(min(int64_t(kVec), max(int64_t(0), -e))), int(max(int64_t(0), min(int64_t(kVec), len - e)))};
+}
+
+template <int TYPE>
+__device__ __forceinline__ Vec<TYPE> load(const void *base, int64_t e, Some n)
+{
+    typedef Raw<TYPE, kVec> R;
+    const GLOBAL typename R::elem *p = (const GLOBAL typename R::elem *)base + e;
+    if (n.all()) return __builtin_nontemporal_load((const GLOBAL typename R::any *)p);
+    Vec<TYPE> x = 0;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+        if (j >= n.lo && j < n.hi) x[j] = p[j];
+    return x;
+}
+
+template <int TYPE>
+__device__ __forceinline__ void store(void *base, int64_t e, Some n, const float (&v)[kVec])
+{
+    typedef Raw<TYPE, kVec> R;
+    GLOBAL typename R::elem *p = (GLOBAL typename R::elem *)base + e;
+    Vec<TYPE> x;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) x[j] = narrow<TYPE>(v[j]);
+    if (n.all()) {
+        __builtin_nontemporal_store(x, (GLOBAL typename R::any *)p);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (j >= n.lo && j < n.hi) p[j] = x[j];
+    }
+}
+
+// What a step multiplies with, the same for all elements.
+struct Scalars {
+    float f, b1, a1, b2, a2, eps, size, root;
+    double lr;
+};
+
+// False: the step is left out.
+__device__ __forceinline__ bool scalars_of(const AdamArgs &a, Scalars *c)
+{
+    *c = {1.0f, a.b1, a.a1, a.b2, a.a2, a.eps, a.size, a.root, a.lr};
+    if (a.norm) {
+        const float n = *(const CONSTANT float *)a.norm;
+        if (a.skip && !(fabsf(n) < INFINITY)) return false;
+        if (a.max_norm < INFINITY) {
+            const float f = __fdiv_rn(a.max_norm, __fadd_rn(n, 1e-6f));
+            c->f = f >= 1.0f ? 1.0f : f;   // a NaN stays one
+        }
+    }
+    if (a.lr_ptr || a.step_ptr) {
+        if (a.lr_ptr) c->lr = double(*(const CONSTANT float *)a.lr_ptr);
+        const int64_t t = a.step_ptr ? max(int64_t(1), *(const CONSTANT int64_t *)a.step_ptr) : a.step;
+        c->size = float(c->lr / (1.0 - power(a.beta1, t)));
+        c->root = float(1.0 / __builtin_sqrt(1.0 - power(a.beta2, t)));
+    }
+    return true;
+}
+
+// One element's step; returns sqrt(v).
+__device__ __forceinline__ float update(const Scalars &c, float keep, float g, float &m, float &v, float &p)
+{
+    g = __fmul_rn(g, c.f);
+    m = __fadd_rn(__fmul_rn(m, c.b1), __fmul_rn(g, c.a1));
+    v = __fadd_rn(__fmul_rn(v, c.b2), __fmul_rn(__fmul_rn(g, g), c.a2));
+    const float r = sqrtf(v);
+    const float d = m / __fadd_rn(__fmul_rn(r, c.root), c.eps);
+    p = __fsub_rn(__fmul_rn(p, keep), __fmul_rn(d, c.size));
+    return r;
+}
+
+template <int GRAD, AdamOut OUT>
+struct Types {
+    static constexpr int param = OUT == kParamBF16 ? DDP_BF16 : OUT == kParamF16 ? DDP_F16 : DDP_F32;
+    static constexpr int copy = OUT == kParamF32CopyBF16 ? DDP_BF16 : OUT == kParamF32CopyF16 ? DDP_F16 : -1;
+};
+
+template <int GRAD, AdamOut OUT, bool FULL>
+__device__ __forceinline__ void step_32(const CONSTANT AdamSeg &s, int64_t base, const Scalars &c, float keep)
+{
+    typedef Types<GRAD, OUT> T;
+    Vec<GRAD> g[kGroups];
+    Vec<T::param> p[kGroups];
+    Vec<DDP_F32> m[kGroups], v[kGroups];
+    base += int(threadIdx.x) * kVec;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+        const int64_t e = base + k * kThreads * kVec;
+        const Some n = some_of<FULL>(e, s.len);
+        g[k] = load<GRAD>(s.grad, e, n);
+        p[k] = load<T::param>(s.param, e, n);
+        m[k] = load<DDP_F32>(s.m, e, n);
+        v[k] = load<DDP_F32>(s.v, e, n);
+    }
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+        const int64_t e = base + k * kThreads * kVec;
+        const Some n = some_of<FULL>(e, s.len);
+        float x[kVec], y[kVec], z[kVec];
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            x[j] = widen<T::param>(p[k][j]), y[j] = m[k][j], z[j] = v[k][j];
+            update(c, keep, widen<GRAD>(g[k][j]), y[j], z[j], x[j]);
+        }
+        store<T::param>(s.param, e, n, x);
+        if constexpr (T::copy >= 0) store<T::copy>(s.copy, e, n, x);
+        store<DDP_F32>(s.m, e, n, y);
+        store<DDP_F32>(s.v, e, n, z);
+    }
+}
+
+typedef uint32_t codes_any __attribute__((aligned(1)));
+
+// The codes of four elements, those the tensor has not as zeros.
+__device__ __forceinline__ uint32_t load_codes(const void *base, int64_t e, Some n)
+{
+    const GLOBAL uint8_t *p = (const GLOBAL uint8_t *)base + e;
+    if (n.all()) return __builtin_nontemporal_load((const GLOBAL codes_any *)p);
+    uint32_t x = 0;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+        if (j >= n.lo && j < n.hi) x |= uint32_t(p[j]) << (8 * j);
+    return x;
+}
+
+__device__ __forceinline__ void store_codes(void *base, int64_t e, Some n, uint32_t x)
+{
+    GLOBAL uint8_t *p = (GLOBAL uint8_t *)base + e;
+    if (n.all()) {
+        __builtin_nontemporal_store(x, (GLOBAL codes_any *)p);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (j >= n.lo && j < n.hi) p[j] = uint8_t(x >> (8 * j));
+    }
+}
+
+__device__ __forceinline__ void decode(uint32_t code, float scale, float (&x)[kVec])
+{
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(int(code), false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(int(code), true);
+    x[0] = __fmul_rn(lo[0], scale), x[1] = __fmul_rn(lo[1], scale);
+    x[2] = __fmul_rn(hi[0], scale), x[3] = __fmul_rn(hi[1], scale);
+}
+
+__device__ __forceinline__ uint32_t encode(const float (&x)[kVec])
+{
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
+    return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], w, true));
+}
+
+template <int CONTROL>
+__device__ __forceinline__ uint32_t max_with(uint32_t x)
+{
+    return max(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), CONTROL, 0xf, 0xf, false)));
+}
+
+// The largest of a half wave's values, in each of its lanes.
+__device__ __forceinline__ uint32_t over_half_wave(uint32_t x)
+{
+    x = max_with<0xb1>(x);    // the neighbour
+    x = max_with<0x4e>(x);    // the other pair of four
+    x = max_with<0x141>(x);   // the other four of eight
+    x = max_with<0x140>(x);   // the other eight of sixteen
+    const auto y = __builtin_amdgcn_permlane16_swap(x, x, false, false);   // the other sixteen of thirty-two
+    return max(uint32_t(y[0]), uint32_t(y[1]));
+}
+
+// Of a block's largest magnitude: what its values are multiplied with before
+// they are rounded to codes, and the scale that undoes it. A block whose
+// largest is below 2^-100, whose 448 / top could overflow, is held as zeros.
+struct BlockScale {
+    float up, down;
+    __device__ __forceinline__ explicit BlockScale(uint32_t top_bits)
+    {
+        const float top = __uint_as_float(top_bits);
+        const bool none = top < 0x1p-100f;
+        up = none ? 0.0f : 448.0f / top;
+        down = none ? 0.0f : top / 448.0f;
+    }
+};
+
+static_assert(kStateBlock == 1 << 7, "blocks are found by shifts");
+
+template <int GRAD, AdamOut OUT, bool FULL>
+__device__ __forceinline__ void step_8(const CONSTANT AdamSeg &s, int64_t base, const Scalars &c, float keep)
+{
+    typedef Types<GRAD, OUT> T;
+    Vec<GRAD> g[kGroups];
+    Vec<T::param> p[kGroups];
+    uint32_t m[kGroups], v[kGroups];
+    float ms[kGroups], vs[kGroups];
+    base += int(threadIdx.x) * kVec;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+        const int64_t e = base + k * kThreads * kVec;
+        const Some n = some_of<FULL>(e, s.len);
+        // a block that begins inside the tensor has a scale
+        const int64_t block = e >> 7;
+        const bool has = FULL || block << 7 < s.len;
+        ms[k] = has ? ((const GLOBAL float *)s.m_scale)[block] : 0.0f;
+        vs[k] = has ? ((const GLOBAL float *)s.v_scale)[block] : 0.0f;
+        m[k] = load_codes(s.m, e, n);
+        v[k] = load_codes(s.v, e, n);
+        g[k] = load<GRAD>(s.grad, e, n);
+        p[k] = load<T::param>(s.param, e, n);
+    }
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+        const int64_t e = base + k * kThreads * kVec;
+        const Some n = some_of<FULL>(e, s.len);
+        float x[kVec], y[kVec], r[kVec];
+        decode(m[k], ms[k], y);
+        decode(v[k], vs[k], r);
+        uint32_t top_m = 0, top_r = 0;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            x[j] = widen<T::param>(p[k][j]);
+            float z = __fmul_rn(r[j], r[j]);
+            r[j] = update(c, keep, widen<GRAD>(g[k][j]), y[j], z, x[j]);
+            top_m = max(top_m, __float_as_uint(y[j]) & 0x7fffffffu);
+            top_r = max(top_r, __float_as_uint(r[j]) & 0x7fffffffu);
+        }
+        store<T::param>(s.param, e, n, x);
+        if constexpr (T::copy >= 0) store<T::copy>(s.copy, e, n, x);
+        const BlockScale bm(over_half_wave(top_m)), br(over_half_wave(top_r));
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            y[j] = __fmul_rn(y[j], bm.up);
+            // 2^-9 is the smallest code
+            r[j] = r[j] > 0.0f ? fmaxf(__fmul_rn(r[j], br.up), 0x1p-9f) : 0.0f;
+        }
+        store_codes(s.m, e, n, encode(y));
+        store_codes(s.v, e, n, encode(r));
+        const int64_t block = e >> 7;
+        if (e % kStateBlock == 0 && (FULL || e < s.len)) {
+            ((GLOBAL float *)s.m_scale)[block] = bm.down;
+            ((GLOBAL float *)s.v_scale)[block] = br.down;
+        }
+    }
+}
+
+template <int BITS, int GRAD, AdamOut OUT>
+__device__ __forceinline__ void step_tile(const CONSTANT AdamSeg &s, int64_t base, const Scalars &c, float keep)
+{
+    const bool full = base >= 0 && base + kAdamTile <= s.len;
+    if (BITS == 32) {
+        if (full)
+            step_32<GRAD, OUT, true>(s, base, c, keep);
+        else
+            step_32<GRAD, OUT, false>(s, base, c, keep);
+    } else {
+        if (full)
+            step_8<GRAD, OUT, true>(s, base, c, keep);
+        else
+            step_8<GRAD, OUT, false>(s, base, c, keep);
+    }
+}
+
+template <int BITS, int GRAD>
+__device__ __forceinline__ void step_out(const CONSTANT AdamSeg &s, int64_t base, const Scalars &c, float keep)
+{
+    switch (s.out) {
+    case kParamF32: step_tile<BITS, GRAD, kParamF32>(s, base, c, keep); break;
+    case kParamF32CopyBF16: step_tile<BITS, GRAD, kParamF32CopyBF16>(s, base, c, keep); break;
+    case kParamF32CopyF16: step_tile<BITS, GRAD, kParamF32CopyF16>(s, base, c, keep); break;
+    case kParamBF16: step_tile<BITS, GRAD, kParamBF16>(s, base, c, keep); break;
+    default: step_tile<BITS, GRAD, kParamF16>(s, base, c, keep); break;
+    }
+}
+
+template <int BITS>
+__global__ void __launch_bounds__(kThreads) adamw(AdamTables t, AdamArgs a, int first)
+{
+    const int tile = first + int(blockIdx.x);
+    const CONSTANT AdamSeg &s = ((const CONSTANT AdamSeg *)t.segs)[((const CONSTANT int32_t *)t.tile_seg)[tile]];
+    Scalars c;
+    if (!scalars_of(a, &c)) return;
+    const int64_t base = int64_t(tile - s.tile0) * kAdamTile - s.shift;
+    const float keep = float(1.0 - c.lr * s.decay);
+    if (s.type == DDP_F32)
+        step_out<BITS, DDP_F32>(s, base, c, keep);
+    else if (s.type == DDP_BF16)
+        step_out<BITS, DDP_BF16>(s, base, c, keep);
+    else
+        step_out<BITS, DDP_F16>(s, base, c, keep);
+}
+
+// Tiles of one launch: its grid holds 2^32 threads.
+constexpr int32_t kMostTiles = int32_t(1) << 23;
+
+}  // namespace
+
+hipError_t launch_adamw(const AdamTables &t, const AdamArgs &a, hipStream_t s)
+{
+    for (int32_t first = 0; first < t.tiles; first += kMostTiles) {
+        const dim3 g(static_cast<unsigned>(std::min(kMostTiles, t.tiles - first))), b(kThreads);
+        if (t.bits == 32)
+            hipLaunchKernelGGL(adamw<32>, g, b, 0, s, t, a, first);
+        else
+            hipLaunchKernelGGL(adamw<8>, g, b, 0, s, t, a, first);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace ddp

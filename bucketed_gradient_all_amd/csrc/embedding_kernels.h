@@ -3,6 +3,7 @@
 #pragma once
 
 #include "../../include/ddp.h"
+#include "element.h"
 #include "embedding.h"
 
 #include <hip/hip_runtime.h>
@@ -11,51 +12,6 @@
 
 namespace ddp {
 namespace {
-
-#define GLOBAL __attribute__((address_space(1)))
-
-// VEC elements of a type as they lie in memory, at any element's address.
-template <int TYPE, int VEC>
-struct Raw;
-template <int VEC>
-struct Raw<DDP_F32, VEC> {
-    typedef float type __attribute__((ext_vector_type(VEC)));
-    typedef type any __attribute__((aligned(4)));
-    typedef float elem;
-};
-template <int VEC>
-struct Raw<DDP_BF16, VEC> {
-    typedef unsigned short type __attribute__((ext_vector_type(VEC)));
-    typedef type any __attribute__((aligned(2)));
-    typedef unsigned short elem;
-};
-template <int VEC>
-struct Raw<DDP_F16, VEC> : Raw<DDP_BF16, VEC> {};
-
-template <int TYPE, class E>
-__device__ __forceinline__ float widen(E v)
-{
-    if constexpr (TYPE == DDP_F32)
-        return v;
-    else if constexpr (TYPE == DDP_BF16)
-        return __uint_as_float(uint32_t(v) << 16);
-    else
-        return float(__builtin_bit_cast(_Float16, v));
-}
-
-// One rounding to the type, to nearest even; beyond fp16's range it is inf.
-template <int TYPE>
-__device__ __forceinline__ typename Raw<TYPE, 1>::elem narrow(float v)
-{
-    if constexpr (TYPE == DDP_F32) {
-        return v;
-    } else if constexpr (TYPE == DDP_BF16) {
-        return __builtin_bit_cast(unsigned short, static_cast<__bf16>(v));
-    } else {
-        asm volatile("" : "+v"(v));   // an fp32 value before the conversion (see `wire` in reduce_kernels.h)
-        return __builtin_bit_cast(unsigned short, static_cast<_Float16>(v));
-    }
-}
 
 // STREAM: read past the caches.
 template <int TYPE, int VEC, bool STREAM = false>
@@ -110,10 +66,6 @@ __device__ __forceinline__ void store(void *base, int64_t e, const float (&v)[VE
             if (j >= skip) *(GLOBAL typename R::elem *)(p + j) = narrow<TYPE>(v[j]);
     }
 }
-
-// Data that no wave of the launch writes: uniform loads of it go through the
-// scalar cache.
-#define CONSTANT __attribute__((address_space(4)))
 
 // The row of a token, or -1.
 __device__ __forceinline__ int row_of(const EmbeddingArgs &a, int64_t tok)

@@ -2,6 +2,7 @@
 // launches of the norm and of clipping.
 #include "grad_list.h"
 #include "host_common.h"
+#include "spans.h"
 
 #include <algorithm>
 #include <cmath>
@@ -16,24 +17,8 @@ using ddp::GradTables;
 using ddp::guarded;
 using ddp::hip_fail;
 using ddp::kGradTile;
-
-namespace {
-
-// Addresses [lo, hi).
-struct Span {
-    uintptr_t lo, hi;
-};
-
-// Sorted and apart.
-using Spans = std::vector<Span>;
-
-bool meets(const Spans &v, uintptr_t lo, uintptr_t hi)
-{
-    const auto it = std::partition_point(v.begin(), v.end(), [lo](const Span &s) { return s.hi <= lo; });
-    return it != v.end() && it->lo < hi;
-}
-
-}  // namespace
+using ddp::meets;
+using ddp::Spans;
 
 struct ddp_grads {
     GradTables tables{};

@@ -1,6 +1,6 @@
 /* ddp.h — bucketed gradient reduction for data-parallel training, MI355X (gfx950):
- * the reduction, the norm and clipping of its results, and the embedding's
- * lookup and gradient.
+ * the reduction, the norm and clipping of its results, the AdamW step, and the
+ * embedding's lookup and gradient.
  *
  * C ABI of libddp.so. Plain pointers and sizes only; every function returns
  * an int status (DDP_OK = 0, negative on error, text in ddp_last_error())
@@ -545,6 +545,106 @@ int ddp_clip_grad_norm(const ddp_grads *g, int32_t norm_type, float max_norm, fl
  * several ranks' lists, summed. Errors as ddp_clip_grad_norm, but norm may
  * lie anywhere except where the call writes. */
 int ddp_clip_grads(const ddp_grads *g, float max_norm, const float *norm, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * AdamW: the optimizer's step over many tensors at once.
+ *
+ * What follows the reduction and the norm: every parameter takes its step from
+ * its reduced gradient, a whole model's or the shard of an owner after a
+ * reduce-scatter ([MegatronDDP §3]: chunk c of a bucket, its place in the
+ * owner's flat buffer is the gradient's pointer). A list names the tensors
+ * once; a step is one launch however many tensors it holds, reads and writes
+ * every value once, and clips the gradients by a given norm on the way, so that
+ * neither ddp_clip_grad_norm's pass nor scaled gradients are needed.
+ * ------------------------------------------------------------------------- */
+enum {
+    DDP_STATE_F32 = 0,    /* both moments in fp32                                                         */
+    DDP_STATE_8BIT = 1    /* both in 8 bits, with one fp32 scale for each DDP_STATE_BLOCK elements: the
+                             first moment m, and the root r of the second, as e4m3 codes of
+                             m * (448 / max|m|) and r * (448 / max r) (round to nearest even; a positive r
+                             has at least the smallest positive code). m is code * scale, the second moment
+                             (code * scale)^2. All codes and scales zero is the state before the first step.
+                             A block whose max|m| is below 2^-100 is held as zeros; an infinity or a NaN
+                             among a block's gradients leaves none of its states finite                   */
+};
+#define DDP_STATE_BLOCK 128
+
+typedef struct ddp_adamw ddp_adamw;   /* opaque, owned by the library */
+
+typedef struct {
+    int32_t n_tensors;           /* N >= 0                                                          */
+    int32_t state;               /* DDP_STATE_*, of all tensors                                     */
+    const int64_t *numel;        /* [N] elements, >= 0                                              */
+    const int32_t *grad_dtype;   /* [N] DDP_F32, DDP_BF16 or DDP_F16; NULL: all fp32                */
+    const int32_t *param_dtype;  /* [N] the same of the parameters                                  */
+    const void *const *grads;    /* [N] device pointers; like all of the desc's at any multiple of the
+                                    element's size (codes: anywhere), contiguous; of a tensor of no
+                                    elements no pointer is looked at                                */
+    void *const *params;         /* [N] stepped in place. 16-bit parameters are widened, stepped in
+                                    fp32 and rounded once                                           */
+    void *const *copies;         /* [N] where the stepped fp32 parameters are also written in 16 bits
+                                    (what the next forward reads), NULL entries: nowhere; or NULL   */
+    const int32_t *copy_dtype;   /* [N] DDP_BF16 or DDP_F16 for each copy; given exactly with copies */
+    void *const *m;              /* [N] first moments: fp32, or codes of one byte                   */
+    void *const *v;              /* [N] second moments, the same                                    */
+    float *const *m_scale;       /* [N] 8-bit states: ceil(numel / DDP_STATE_BLOCK) scales, block b
+                                    that of the elements from b * DDP_STATE_BLOCK on; else not read */
+    float *const *v_scale;
+    const double *weight_decay;  /* [N] decay of each tensor, finite and >= 0; NULL: none           */
+    void *workspace;             /* device memory of ddp_adamw_workspace_bytes() bytes, 16-byte
+                                    aligned, for the list's tables                                  */
+    size_t workspace_bytes;
+} ddp_adamw_desc;
+
+/* Device workspace a list needs for its tables (80 bytes a tensor, 4 bytes per
+ * 2048 elements). Returns 0 and sets ddp_last_error() if the desc is invalid;
+ * pointers are not looked at. */
+size_t ddp_adamw_workspace_bytes(const ddp_adamw_desc *desc);
+
+/* Builds the list's tables and uploads them (synchronously) into the
+ * workspace, as ddp_grads_create does, under the same rules: workspace and
+ * tensors stay valid for as long as the list, or a graph that recorded a step,
+ * is used; not while a stream is being recorded; tied to the device that is
+ * current here. *out is set only on success.
+ * Errors: DDP_ERR_INVALID: bad sizes, types, decays or alignment; a copy
+ * beside 16-bit parameters; any two of the tensors' ranges, or one and the
+ * workspace, that overlap; DDP_ERR_HIP; DDP_ERR_NOMEM. */
+int ddp_adamw_create(const ddp_adamw_desc *desc, ddp_adamw **out);
+
+/* Releases the list's host state; touches no device memory. The workspace
+ * must outlive the steps still queued. NULL is a no-op. */
+int ddp_adamw_destroy(ddp_adamw *o);
+
+typedef struct {
+    double lr;                /* finite, >= 0                                                       */
+    double beta1, beta2;      /* in [0, 1)                                                          */
+    double eps;               /* finite, >= 0                                                       */
+    int64_t step;             /* t, the number of this step, from 1 on                              */
+    const float *lr_ptr;      /* device, one float that the step reads instead of lr; or NULL. With it
+                                 and step_ptr the replays of a recorded step go on with the schedule */
+    const int64_t *step_ptr;  /* device, one count read instead of step (below 1 counts as 1); NULL */
+    const float *norm;        /* device, one float: the norm the gradients are clipped by, as
+                                 ddp_grad_norm leaves it; NULL: they are taken as they are           */
+    float max_norm;           /* >= 0; infinite: not clipped. Read only with norm                   */
+    int32_t skip_nonfinite;   /* != 0: a norm that is not finite leaves everything as it was; needs
+                                 norm                                                               */
+} ddp_adamw_args;
+
+/* One step of every tensor, on `stream`:
+ *   g = grad * f,  f = min(1, max_norm / (norm + 1e-6)), or 1 without a norm
+ *   m = beta1 * m + (1 - beta1) * g
+ *   v = beta2 * v + (1 - beta2) * g^2
+ *   p = p * (1 - lr * weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32, each operation rounded by itself; the factors that no element
+ * enters (powers, 1 - lr * weight_decay) in 64 bits and rounded once. Without
+ * skip_nonfinite a norm that is not finite goes into the gradients as in
+ * ddp_clip_grad_norm. Gradients are only read. Steps of one list change its
+ * tensors and must not run at once; otherwise a list is only read, from any
+ * stream and replayed graph. May be recorded into a HIP graph.
+ * Errors: DDP_ERR_INVALID (args out of the ranges above, a device scalar that
+ * is misaligned or lies where the step writes, another device current than
+ * the list's, a stream of another device), DDP_ERR_HIP. */
+int ddp_adamw_step(const ddp_adamw *o, const ddp_adamw_args *args, void *stream);
 
 /* ---------------------------------------------------------------------------
  * Embedding: the lookup of a table's rows, and the table's gradient.
