@@ -1,6 +1,7 @@
 """Python binding of libddp.so (include/ddp.h): bucketed gradient reduction
 for data-parallel training on MI355X (gfx950), the norm and clipping of the
-gradients, the AdamW step, and the embedding's lookup and gradient.
+gradients, the AdamW step, the embedding's lookup and gradient, and the layer
+norm's two passes.
 
 Argument marshalling only: every step of the path runs in the C++ host
 library and its HIP kernels. The functions keep the C names; a negative
@@ -63,16 +64,19 @@ DDP_STATE_BLOCK = 128
 DDP_I32 = 0
 DDP_I64 = 1
 
+DDP_LAYER_NORM = 0
+DDP_RMS_NORM = 1
+
 HIPCC_FLAGS = ["--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17",
                "-ffp-contract=off", "-fno-fast-math",
                "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 
 # one object per source; the kernel families compile in parallel
-SOURCES = ["reducer.cpp", "grad_list.cpp", "embedding.cpp", "adamw.cpp", "bucket_reduce.hip", "bucket_bf16_hook.hip",
-           "bucket_fp16_hook.hip", "static_tables.hip", "grad_norm.hip", "embedding.hip",
-           "embedding_small.hip", "adamw.hip"]
+SOURCES = ["reducer.cpp", "grad_list.cpp", "embedding.cpp", "adamw.cpp", "layernorm.cpp",
+           "bucket_reduce.hip", "bucket_bf16_hook.hip", "bucket_fp16_hook.hip", "static_tables.hip", "grad_norm.hip",
+           "embedding.hip", "embedding_small.hip", "adamw.hip", "layernorm.hip", "layernorm_grad.hip"]
 HEADERS = ["host_common.h", "internal.h", "reduce_kernels.h", "static_area.h", "grad_list.h", "embedding.h",
-           "embedding_kernels.h", "element.h", "spans.h", "adamw.h"]
+           "embedding_kernels.h", "element.h", "spans.h", "adamw.h", "layernorm.h", "layernorm_kernels.h"]
 
 
 BUILD_DIR = os.path.join(HERE, "_build")
@@ -213,6 +217,22 @@ class ddp_embedding_desc(ctypes.Structure):
     ]
 
 
+class ddp_layernorm_desc(ctypes.Structure):
+    _fields_ = [
+        ("width", ctypes.c_int64),
+        ("x_stride", ctypes.c_int64),
+        ("add_stride", ctypes.c_int64),
+        ("z_stride", ctypes.c_int64),
+        ("y_stride", ctypes.c_int64),
+        ("eps", ctypes.c_float),
+        ("kind", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("y_dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("grad_dtype", ctypes.c_int32),
+    ]
+
+
 _lib = None
 
 
@@ -259,6 +279,8 @@ def lib():
             "ddp_adamw_step": [P, ctypes.POINTER(ddp_adamw_args), P],
             "ddp_embedding_lookup": [ctypes.POINTER(ddp_embedding_desc), P, P, I64, P, P],
             "ddp_embedding_grad": [ctypes.POINTER(ddp_embedding_desc), P, P, I64, P, I32, P, SIZE, P],
+            "ddp_layernorm": [ctypes.POINTER(ddp_layernorm_desc), I64, P, P, P, P, P, P, P, P, P],
+            "ddp_layernorm_grad": [ctypes.POINTER(ddp_layernorm_desc), I64, P, P, P, P, P, P, P, P, P, I32, P, SIZE, P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -268,7 +290,8 @@ def lib():
                            "ddp_grads_workspace_bytes": [ctypes.POINTER(ddp_grads_desc)],
                            "ddp_reducer_grads_workspace_bytes": [P],
                            "ddp_adamw_workspace_bytes": [ctypes.POINTER(ddp_adamw_desc)],
-                           "ddp_embedding_grad_workspace_bytes": [ctypes.POINTER(ddp_embedding_desc), I64]}.items():
+                           "ddp_embedding_grad_workspace_bytes": [ctypes.POINTER(ddp_embedding_desc), I64],
+                           "ddp_layernorm_grad_workspace_bytes": [ctypes.POINTER(ddp_layernorm_desc), I64]}.items():
             f = getattr(L, name)
             f.argtypes = args
             f.restype = ctypes.c_size_t
@@ -972,4 +995,43 @@ def ddp_embedding_grad_workspace_bytes(desc: EmbeddingDesc, n_tokens: int) -> in
 def ddp_embedding_grad(desc: EmbeddingDesc, dout: int, tokens: int, n_tokens: int, grad: int, accumulate: bool,
                        workspace: int, workspace_bytes: int, stream: int) -> None:
     _check(lib().ddp_embedding_grad(ctypes.byref(desc.c), dout or None, tokens or None, n_tokens, grad or None,
+                                    1 if accumulate else 0, workspace or None, workspace_bytes, stream or None))
+
+
+class LayerNormDesc:
+    """A ddp_layernorm_desc; strides default to the width."""
+
+    def __init__(self, width: int, kind: int = DDP_LAYER_NORM, x_dtype: int = DDP_F32, y_dtype: Optional[int] = None,
+                 weight_dtype: int = DDP_F32, grad_dtype: int = DDP_F32, eps: float = 1e-5,
+                 x_stride: Optional[int] = None, add_stride: Optional[int] = None, z_stride: Optional[int] = None,
+                 y_stride: Optional[int] = None):
+        d = ddp_layernorm_desc()
+        d.width, d.eps, d.kind = width, eps, kind
+        d.x_stride = width if x_stride is None else x_stride
+        d.add_stride = width if add_stride is None else add_stride
+        d.z_stride = width if z_stride is None else z_stride
+        d.y_stride = width if y_stride is None else y_stride
+        d.x_dtype, d.y_dtype = x_dtype, x_dtype if y_dtype is None else y_dtype
+        d.weight_dtype, d.grad_dtype = weight_dtype, grad_dtype
+        self.c = d
+
+
+def ddp_layernorm(desc: LayerNormDesc, n_rows: int, x: int, weight: int, bias: int, y: int, stream: int, add: int = 0,
+                  z: int = 0, mean: int = 0, rstd: int = 0) -> None:
+    _check(lib().ddp_layernorm(ctypes.byref(desc.c), n_rows, x or None, add or None, weight or None, bias or None,
+                               z or None, y or None, mean or None, rstd or None, stream or None))
+
+
+def ddp_layernorm_grad_workspace_bytes(desc: LayerNormDesc, n_rows: int) -> int:
+    n = lib().ddp_layernorm_grad_workspace_bytes(ctypes.byref(desc.c), n_rows)
+    if n == 0:
+        raise DDPError(DDP_ERR_INVALID, ddp_last_error())
+    return int(n)
+
+
+def ddp_layernorm_grad(desc: LayerNormDesc, n_rows: int, dy: int, z: int, weight: int, mean: int, rstd: int, dx: int,
+                       dweight: int, dbias: int, accumulate: bool, workspace: int, workspace_bytes: int, stream: int,
+                       dz: int = 0) -> None:
+    _check(lib().ddp_layernorm_grad(ctypes.byref(desc.c), n_rows, dy or None, z or None, dz or None, weight or None,
+                                    mean or None, rstd or None, dx or None, dweight or None, dbias or None,
                                     1 if accumulate else 0, workspace or None, workspace_bytes, stream or None))

@@ -2,6 +2,7 @@
 // and the launches.
 #include "embedding.h"
 #include "host_common.h"
+#include "spans.h"
 
 #include <algorithm>
 #include <cmath>
@@ -12,6 +13,7 @@ using ddp::EmbeddingWork;
 using ddp::fail;
 using ddp::guarded;
 using ddp::hip_fail;
+using ddp::rows_meet;
 
 namespace {
 
@@ -226,19 +228,6 @@ int lookup(const ddp_embedding_desc *d, const void *table, const void *tokens, i
     if (rc != DDP_OK) return rc;
     const hipError_t e = ddp::launch_lookup(args_of(*d, n), table, tokens, out, s);
     return e == hipSuccess ? DDP_OK : hip_fail("embedding lookup", e);
-}
-
-// Whether one of n rows of `bytes` bytes, `stride` bytes apart, the first at p,
-// meets [lo, hi).
-bool rows_meet(const void *p, int64_t n, int64_t stride, int64_t bytes, uintptr_t lo, uintptr_t hi)
-{
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-    uintptr_t first = 0;   // the first row that ends past lo
-    if (lo >= at + uintptr_t(bytes)) {
-        if (stride == 0) return false;
-        first = (lo - at - uintptr_t(bytes)) / uintptr_t(stride) + 1;
-    }
-    return first < uintptr_t(n) && at + first * uintptr_t(stride) < hi;
 }
 
 // The sum takes rows and positions from the workspace as they stand there:

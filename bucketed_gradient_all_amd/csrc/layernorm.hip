@@ -1,0 +1,214 @@
+// The layer norm's forward pass.
+//
+//   z    = R(x + add), or x
+//   mean = sum z / H                          0 for DDP_RMS_NORM
+//   rstd = 1 / sqrt(sum (z - mean)^2 / H + eps)
+//   y    = R((z - mean) * rstd * weight + bias)
+//
+// One pass over memory: a row stays in the registers of one wave, or of a
+// workgroup where it is wider, between its statistics and its output, so the
+// kernel is bound by memory. Sums are fp32 over the row's threads, then over
+// the wave by cross-lane adds.
+//   * The mean is corrected: sum (z - m) / H for the rounded mean m of the first
+//     sum is added to it, and taken off the squares' sum. It costs one addition
+//     an element and keeps rows exact that lie far from zero.
+#include "layernorm_kernels.h"
+
+namespace ddp {
+namespace {
+
+// z's columns from x's and add's.
+template <int X, int VEC>
+__device__ __forceinline__ void load_z(const LayerForward &f, const void *x, const void *add, const Columns<VEC> &c,
+                                       float (&v)[VEC])
+{
+    widen_all<X, VEC>(load<X, VEC>(x, c.col), v);
+    if (f.add) {
+        float w[VEC];
+        widen_all<X, VEC>(load<X, VEC>(add, c.col), w);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[j] = widen<X>(narrow<X>(v[j] + w[j]));
+    }
+}
+
+// The mean's correction and the deviation from a row's second sums.
+struct Stats {
+    float shift;   // added to the rounded mean
+    float rstd;
+    __device__ __forceinline__ Stats(float sum, float squares, const LayerArgs &a)
+    {
+        const float h = float(a.width);
+        shift = a.rms ? 0.0f : sum / h;
+        const float variance = squares / h - shift * shift;
+        rstd = 1.0f / sqrtf((variance < 0.0f ? 0.0f : variance) + a.eps);   // a NaN stays one
+    }
+};
+
+// A row in the registers of T threads, U vectors each.
+template <int X, int Y, int T, int U, int VEC>
+__global__ void __launch_bounds__(threads_of(T)) layernorm_rows(LayerArgs a, LayerForward f, int64_t first)
+{
+    const int group = T == 64 ? __builtin_amdgcn_readfirstlane(int(threadIdx.x) / 64) : 0;
+    const int64_t row = first + int64_t(blockIdx.x) * (threads_of(T) / T) + group;
+    if (row >= a.rows) return;   // whole waves, and no workgroup that shares a row
+    const int t = int(threadIdx.x) % T;
+    const void *x = row_of<X>(f.x, row, a.x_stride), *add = row_of<X>(f.add, row, a.add_stride);
+    float v[U][VEC];
+#pragma unroll
+    for (int u = 0; u < U; ++u) load_z<X, VEC>(f, x, add, Columns<VEC>(u * T + t, a.width), v[u]);
+    if (f.z) {
+        void *z = row_of<X>(f.z, row, a.z_stride);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const Columns<VEC> c(u * T + t, a.width);
+            if (c.skip < VEC) store<X, VEC>(z, c.col, v[u], c.skip);
+        }
+    }
+    int turn = 0;
+    float mean = 0.0f;
+    if (!a.rms) {
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const Columns<VEC> c(u * T + t, a.width);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) s[0] += j >= c.skip ? v[u][j] : 0.0f;
+        }
+        row_sum<T>(s, turn);
+        mean = s[0] / float(a.width);
+    }
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const Columns<VEC> c(u * T + t, a.width);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            v[u][j] = j >= c.skip ? v[u][j] - mean : 0.0f;
+            s[0] += v[u][j];
+            s[1] = __fmaf_rn(v[u][j], v[u][j], s[1]);
+        }
+    }
+    row_sum<T>(s, turn);
+    const Stats k(s[0], s[1], a);
+    if (t == 0) {
+        if (f.mean) ((GLOBAL float *)f.mean)[row] = mean + k.shift;
+        if (f.rstd) ((GLOBAL float *)f.rstd)[row] = k.rstd;
+    }
+    void *y = row_of<Y>(f.y, row, a.y_stride);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const Columns<VEC> c(u * T + t, a.width);
+        float w[VEC], b[VEC];
+        load_weight<VEC>(f.weight, a.weight_dtype, c.col, 1.0f, w);
+        load_weight<VEC>(f.bias, a.weight_dtype, c.col, 0.0f, b);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) w[j] = __fmaf_rn((v[u][j] - k.shift) * k.rstd, w[j], b[j]);
+        if (c.skip < VEC) store<Y, VEC>(y, c.col, w, c.skip);
+    }
+}
+
+// A row of any width by a workgroup, read again for each pass: from z once it
+// is written, which may lie where x or add does. A thread uses only columns
+// that it wrote itself. Its sums are 64 bits: they may be long.
+template <int X, int Y, int VEC>
+__global__ void __launch_bounds__(1024) layernorm_wide(LayerArgs a, LayerForward f, int64_t first)
+{
+    constexpr int T = 1024;
+    const int64_t row = first + blockIdx.x;
+    const void *x = row_of<X>(f.x, row, a.x_stride), *add = row_of<X>(f.add, row, a.add_stride);
+    void *z = f.z ? row_of<X>(f.z, row, a.z_stride) : nullptr;
+    const int64_t vectors = (a.width + VEC - 1) / VEC;
+    const auto again = [&](const Columns<VEC> &c, float (&v)[VEC]) {
+        if (z)
+            widen_all<X, VEC>(load<X, VEC>(z, c.col), v);
+        else
+            load_z<X, VEC>(f, x, add, c, v);
+    };
+    int turn = 0;
+    float v[VEC];
+    float m[1] = {0.0f};
+    if (z || !a.rms) {
+        double sum = 0.0;
+        for (int64_t i = threadIdx.x; i < vectors; i += T) {
+            const Columns<VEC> c(i, a.width);
+            load_z<X, VEC>(f, x, add, c, v);
+            if (z) store<X, VEC>(z, c.col, v, c.skip);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sum += j >= c.skip ? double(v[j]) : 0.0;
+        }
+        m[0] = float(sum);
+        row_sum<T>(m, turn);
+    }
+    const float mean = a.rms ? 0.0f : m[0] / float(a.width);
+    double sum = 0.0, squares = 0.0;
+    for (int64_t i = threadIdx.x; i < vectors; i += T) {
+        const Columns<VEC> c(i, a.width);
+        again(c, v);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            const double d = j >= c.skip ? double(v[j] - mean) : 0.0;
+            sum += d;
+            squares = __fma_rn(d, d, squares);
+        }
+    }
+    float s[2] = {float(sum), float(squares)};
+    row_sum<T>(s, turn);
+    const Stats k(s[0], s[1], a);
+    if (threadIdx.x == 0) {
+        if (f.mean) ((GLOBAL float *)f.mean)[row] = mean + k.shift;
+        if (f.rstd) ((GLOBAL float *)f.rstd)[row] = k.rstd;
+    }
+    void *y = row_of<Y>(f.y, row, a.y_stride);
+    for (int64_t i = threadIdx.x; i < vectors; i += T) {
+        const Columns<VEC> c(i, a.width);
+        float w[VEC], b[VEC];
+        again(c, v);
+        load_weight<VEC>(f.weight, a.weight_dtype, c.col, 1.0f, w);
+        load_weight<VEC>(f.bias, a.weight_dtype, c.col, 0.0f, b);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) w[j] = __fmaf_rn((v[j] - mean - k.shift) * k.rstd, w[j], b[j]);
+        store<Y, VEC>(y, c.col, w, c.skip);
+    }
+}
+
+// A launch covers rows in order, as many as its grid holds.
+template <class F>
+hipError_t over_rows(int64_t rows, int64_t each, F &&launch)
+{
+    for (int64_t first = 0; first < rows; first += kMostGroups * each) {
+        launch(dim3(static_cast<unsigned>(std::min(kMostGroups, (rows - first + each - 1) / each))), first);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+template <int X, int Y, int T, int U, int VEC>
+hipError_t run_rows(const LayerArgs &a, const LayerForward &f, hipStream_t s)
+{
+    return over_rows(a.rows, threads_of(T) / T, [&](dim3 g, int64_t first) {
+        hipLaunchKernelGGL((layernorm_rows<X, Y, T, U, VEC>), g, dim3(threads_of(T)), 0, s, a, f, first);
+    });
+}
+
+}  // namespace
+
+hipError_t launch_layernorm(const LayerArgs &a, const LayerForward &f, hipStream_t s)
+{
+    return by_types(a, [&](auto x, auto y) {
+        constexpr int X = x(), Y = y(), VEC = layer_vector(X, Y);
+        if (a.width < VEC) return run_rows<X, Y, 64, 1, 1>(a, f, s);
+        const int64_t vectors = (a.width + VEC - 1) / VEC;
+        if (vectors <= 64) return run_rows<X, Y, 64, 1, VEC>(a, f, s);
+        if (vectors <= 128) return run_rows<X, Y, 64, 2, VEC>(a, f, s);
+        if (vectors <= 256) return run_rows<X, Y, 64, 4, VEC>(a, f, s);
+        if (vectors <= 512) return run_rows<X, Y, 64, 8, VEC>(a, f, s);
+        if (vectors <= 1024) return run_rows<X, Y, 256, 4, VEC>(a, f, s);
+        if (vectors <= kRowVectors) return run_rows<X, Y, 1024, 2, VEC>(a, f, s);
+        return over_rows(a.rows, 1, [&](dim3 g, int64_t first) {
+            hipLaunchKernelGGL((layernorm_wide<X, Y, VEC>), g, dim3(1024), 0, s, a, f, first);
+        });
+    });
+}
+
+}  // namespace ddp

@@ -1,0 +1,306 @@
+// The layer norm's backward pass. With hat = (z - mean) * rstd and d = dy * weight,
+//
+//   dx      = R(rstd * (d - sum d / H - hat * sum(d * hat) / H) + dz)
+//   dweight = sum over the rows of dy * hat
+//   dbias   = sum over the rows of dy
+//
+// where DDP_RMS_NORM has no mean and no sum d / H. One pass over memory, bound by
+// it: a row stays in registers between its two sums and dx, and each thread
+// keeps the sums of its columns over all rows that its workgroup takes. Every
+// workgroup leaves one row of such sums (a part), which a second launch adds
+// up: no atomics, and an order that the sizes alone decide.
+#include "layernorm_kernels.h"
+
+namespace ddp {
+namespace {
+
+// hat and d of one vector, zero in the columns that are skipped.
+template <int X, int Y, int VEC>
+__device__ __forceinline__ void normalise(const typename Raw<X, VEC>::type &z, const typename Raw<Y, VEC>::type &dy,
+                                          float mean, float rstd, int skip, float (&hat)[VEC], float (&g)[VEC])
+{
+    widen_all<X, VEC>(z, hat);
+    widen_all<Y, VEC>(dy, g);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        hat[j] = j >= skip ? (hat[j] - mean) * rstd : 0.0f;
+        g[j] = j >= skip ? g[j] : 0.0f;
+    }
+}
+
+// The sums that a row's dx takes off.
+struct Along {
+    float shift, slope;
+    __device__ __forceinline__ Along(float d, float d_hat, const LayerArgs &a)
+    {
+        const float h = float(a.width);
+        shift = a.rms ? 0.0f : d / h;
+        slope = d_hat / h;
+    }
+};
+
+template <int X, int VEC>
+__device__ __forceinline__ void store_dx(const LayerBackward &b, void *dx, const void *dz, const Columns<VEC> &c,
+                                         const float (&d)[VEC], const float (&hat)[VEC], const Along &k, float rstd)
+{
+    float v[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) v[j] = (d[j] - k.shift - hat[j] * k.slope) * rstd;
+    if (b.dz) {
+        float w[VEC];
+        widen_all<X, VEC>(load<X, VEC>(dz, c.col), w);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[j] += w[j];
+    }
+    if (c.skip < VEC) store<X, VEC>(dx, c.col, v, c.skip);
+}
+
+// Rows in the registers of T threads, U vectors each.
+template <int X, int Y, int T, int U, int VEC>
+__global__ void __launch_bounds__(threads_of(T)) layernorm_grad_rows(LayerArgs a, LayerBackward b)
+{
+    constexpr int GROUPS = threads_of(T) / T;
+    const int group = T == 64 ? __builtin_amdgcn_readfirstlane(int(threadIdx.x) / 64) : 0;
+    const int t = int(threadIdx.x) % T;
+    float w[U][VEC], dw[U][VEC] = {}, db[U][VEC] = {};
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        load_weight<VEC>(b.weight, a.weight_dtype, Columns<VEC>(u * T + t, a.width).col, 1.0f, w[u]);
+    int turn = 0;
+    for (int64_t row = int64_t(blockIdx.x) * GROUPS + group; row < a.rows; row += int64_t(b.n_parts) * GROUPS) {
+        const void *z = row_of<X>(b.z, row, a.z_stride), *dy = row_of<Y>(b.dy, row, a.y_stride);
+        const float mean = b.mean ? ((const GLOBAL float *)b.mean)[row] : 0.0f;
+        const float rstd = ((const GLOBAL float *)b.rstd)[row];
+        typename Raw<X, VEC>::type zr[U];
+        typename Raw<Y, VEC>::type gr[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const Columns<VEC> c(u * T + t, a.width);
+            zr[u] = load<X, VEC>(z, c.col);
+            gr[u] = load<Y, VEC>(dy, c.col);
+        }
+        float s[2] = {0.0f, 0.0f};
+        float hat[U][VEC], d[U][VEC];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const Columns<VEC> c(u * T + t, a.width);
+            normalise<X, Y, VEC>(zr[u], gr[u], mean, rstd, c.skip, hat[u], d[u]);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                dw[u][j] = __fmaf_rn(d[u][j], hat[u][j], dw[u][j]);
+                db[u][j] += d[u][j];
+                d[u][j] *= w[u][j];
+                s[0] += d[u][j];
+                s[1] = __fmaf_rn(d[u][j], hat[u][j], s[1]);
+            }
+        }
+        if (!b.dx) continue;
+        row_sum<T>(s, turn);
+        const Along k(s[0], s[1], a);
+        void *dx = row_of<X>(b.dx, row, a.x_stride);
+        const void *dz = row_of<X>(b.dz, row, a.z_stride);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            store_dx<X, VEC>(b, dx, dz, Columns<VEC>(u * T + t, a.width), d[u], hat[u], k, rstd);
+    }
+    if (!b.parts) return;
+    float *part = b.parts + int64_t(blockIdx.x) * 2 * a.width;
+    if constexpr (GROUPS > 1) {
+        // the groups' sums, added in order
+        __shared__ float sums[2][GROUPS][64][VEC];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (u > 0) __syncthreads();
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sums[0][group][t][j] = dw[u][j], sums[1][group][t][j] = db[u][j];
+            __syncthreads();
+            const Columns<VEC> c(u * T + t, a.width);
+            if (group < 2) {
+                float v[VEC];
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    v[j] = sums[group][0][t][j];
+#pragma unroll
+                    for (int k = 1; k < GROUPS; ++k) v[j] += sums[group][k][t][j];
+                }
+                if (c.skip < VEC) store<DDP_F32, VEC>(part + group * a.width, c.col, v, c.skip);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const Columns<VEC> c(u * T + t, a.width);
+            if (c.skip < VEC) {
+                store<DDP_F32, VEC>(part, c.col, dw[u], c.skip);
+                store<DDP_F32, VEC>(part + a.width, c.col, db[u], c.skip);
+            }
+        }
+    }
+}
+
+// dx of a row of any width by a workgroup, read twice. dx may lie where dy or
+// dz does: a thread uses only columns that it writes itself.
+template <int X, int Y, int VEC>
+__global__ void __launch_bounds__(1024) layernorm_grad_wide(LayerArgs a, LayerBackward b, int64_t first)
+{
+    constexpr int T = 1024;
+    const int64_t row = first + blockIdx.x;
+    const void *z = row_of<X>(b.z, row, a.z_stride), *dy = row_of<Y>(b.dy, row, a.y_stride);
+    const void *dz = row_of<X>(b.dz, row, a.z_stride);
+    void *dx = row_of<X>(b.dx, row, a.x_stride);
+    const float mean = b.mean ? ((const GLOBAL float *)b.mean)[row] : 0.0f;
+    const float rstd = ((const GLOBAL float *)b.rstd)[row];
+    const int64_t vectors = (a.width + VEC - 1) / VEC;
+    float hat[VEC], d[VEC];
+    const auto take = [&](const Columns<VEC> &c) {
+        float w[VEC];
+        normalise<X, Y, VEC>(load<X, VEC>(z, c.col), load<Y, VEC>(dy, c.col), mean, rstd, c.skip, hat, d);
+        load_weight<VEC>(b.weight, a.weight_dtype, c.col, 1.0f, w);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) d[j] *= w[j];
+    };
+    double sum = 0.0, along = 0.0;   // may be long
+    for (int64_t i = threadIdx.x; i < vectors; i += T) {
+        take(Columns<VEC>(i, a.width));
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            sum += double(d[j]);
+            along = __fma_rn(double(d[j]), double(hat[j]), along);
+        }
+    }
+    float s[2] = {float(sum), float(along)};
+    int turn = 0;
+    row_sum<T>(s, turn);
+    const Along k(s[0], s[1], a);
+    for (int64_t i = threadIdx.x; i < vectors; i += T) {
+        const Columns<VEC> c(i, a.width);
+        take(c);
+        store_dx<X, VEC>(b, dx, dz, c, d, hat, k, rstd);
+    }
+}
+
+// The parts of rows of any width: a slab of 64 vectors of columns a workgroup,
+// four rows at a time.
+template <int X, int Y, int VEC>
+__global__ void __launch_bounds__(256) layernorm_grad_columns(LayerArgs a, LayerBackward b)
+{
+    constexpr int GROUPS = 4;
+    __shared__ float sums[2][GROUPS][64][VEC];
+    const int group = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / 64), t = int(threadIdx.x) % 64;
+    const Columns<VEC> c(int64_t(blockIdx.x) * 64 + t, a.width);
+    float dw[VEC] = {}, db[VEC] = {};
+    for (int64_t row = int64_t(blockIdx.y) * GROUPS + group; row < a.rows; row += int64_t(b.n_parts) * GROUPS) {
+        const float mean = b.mean ? ((const GLOBAL float *)b.mean)[row] : 0.0f;
+        const float rstd = ((const GLOBAL float *)b.rstd)[row];
+        float hat[VEC], g[VEC];
+        normalise<X, Y, VEC>(load<X, VEC>(row_of<X>(b.z, row, a.z_stride), c.col),
+                             load<Y, VEC>(row_of<Y>(b.dy, row, a.y_stride), c.col), mean, rstd, c.skip, hat, g);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            dw[j] = __fmaf_rn(g[j], hat[j], dw[j]);
+            db[j] += g[j];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) sums[0][group][t][j] = dw[j], sums[1][group][t][j] = db[j];
+    __syncthreads();
+    if (group < 2 && c.skip < VEC) {
+        float v[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            v[j] = sums[group][0][t][j];
+#pragma unroll
+            for (int k = 1; k < GROUPS; ++k) v[j] += sums[group][k][t][j];
+        }
+        store<DDP_F32, VEC>(b.parts + (int64_t(blockIdx.y) * 2 + group) * a.width, c.col, v, c.skip);
+    }
+}
+
+// Sums of the parts, 32 columns a workgroup, each column's parts dealt to 32
+// threads that add theirs in order, and then their sums.
+constexpr int kJoinColumns = 32, kJoinSlices = 32;
+
+__global__ void __launch_bounds__(kJoinColumns *kJoinSlices) layernorm_grad_join(LayerArgs a, LayerBackward b)
+{
+    __shared__ float sums[kJoinSlices][kJoinColumns];
+    const int which = int(blockIdx.y), x = int(threadIdx.x) % kJoinColumns, slice = int(threadIdx.x) / kJoinColumns;
+    void *out = which ? b.dbias : b.dweight;
+    if (!out) return;
+    const int64_t col = int64_t(blockIdx.x) * kJoinColumns + x;
+    float s = 0.0f;
+    if (col < a.width) {
+        const GLOBAL float *p = (const GLOBAL float *)b.parts + which * a.width + col;
+#pragma unroll 8
+        for (int k = slice; k < b.n_parts; k += kJoinSlices) s += p[int64_t(k) * 2 * a.width];
+    }
+    sums[slice][x] = s;
+    __syncthreads();
+    if (slice > 0 || col >= a.width) return;
+    s = sums[0][x];
+#pragma unroll
+    for (int k = 1; k < kJoinSlices; ++k) s += sums[k][x];
+    const auto put = [&](auto type) {
+        typedef Raw<decltype(type)::value, 1> R;
+        GLOBAL typename R::elem *p = (GLOBAL typename R::elem *)out + col;
+        *p = narrow<decltype(type)::value>(b.accumulate ? widen<decltype(type)::value>(*p) + s : s);
+    };
+    if (a.grad_dtype == DDP_F32)
+        put(std::integral_constant<int, DDP_F32>());
+    else if (a.grad_dtype == DDP_BF16)
+        put(std::integral_constant<int, DDP_BF16>());
+    else
+        put(std::integral_constant<int, DDP_F16>());
+}
+
+template <int X, int Y, int T, int U, int VEC>
+hipError_t run_grad(const LayerArgs &a, const LayerBackward &b, hipStream_t s)
+{
+    hipLaunchKernelGGL((layernorm_grad_rows<X, Y, T, U, VEC>), dim3(b.n_parts), dim3(threads_of(T)), 0, s, a, b);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_layernorm_rows(const LayerArgs &a, const LayerBackward &b, hipStream_t s)
+{
+    return by_types(a, [&](auto x, auto y) {
+        constexpr int X = x(), Y = y(), VEC = layer_vector(X, Y);
+        if (a.width < VEC) return run_grad<X, Y, 64, 1, 1>(a, b, s);
+        const int64_t vectors = (a.width + VEC - 1) / VEC;
+        if (vectors <= 64) return run_grad<X, Y, 64, 1, VEC>(a, b, s);
+        if (vectors <= 128) return run_grad<X, Y, 64, 2, VEC>(a, b, s);
+        if (vectors <= 256) return run_grad<X, Y, 256, 1, VEC>(a, b, s);
+        if (vectors <= 512) return run_grad<X, Y, 256, 2, VEC>(a, b, s);
+        if (vectors <= 1024) return run_grad<X, Y, 512, 2, VEC>(a, b, s);
+        return run_grad<X, Y, 1024, 2, VEC>(a, b, s);
+    });
+}
+
+hipError_t launch_layernorm_wide(const LayerArgs &a, const LayerBackward &b, hipStream_t s)
+{
+    return by_types(a, [&](auto x, auto y) {
+        constexpr int X = x(), Y = y(), VEC = layer_vector(X, Y);
+        hipError_t e = hipSuccess;
+        // the sums first: dx may take dy's place
+        if (b.parts) {
+            const dim3 g(static_cast<unsigned>((a.width + 64 * VEC - 1) / (64 * VEC)), static_cast<unsigned>(b.n_parts));
+            hipLaunchKernelGGL((layernorm_grad_columns<X, Y, VEC>), g, dim3(256), 0, s, a, b);
+            e = hipGetLastError();
+        }
+        for (int64_t first = 0; b.dx && e == hipSuccess && first < a.rows; first += kMostGroups) {
+            const dim3 g(static_cast<unsigned>(std::min(kMostGroups, a.rows - first)));
+            hipLaunchKernelGGL((layernorm_grad_wide<X, Y, VEC>), g, dim3(1024), 0, s, a, b, first);
+            e = hipGetLastError();
+        }
+        return e;
+    });
+}
+
+hipError_t launch_layernorm_join(const LayerArgs &a, const LayerBackward &b, hipStream_t s)
+{
+    const dim3 g(static_cast<unsigned>((a.width + kJoinColumns - 1) / kJoinColumns), b.dbias ? 2 : 1);
+    hipLaunchKernelGGL(layernorm_grad_join, g, dim3(kJoinColumns * kJoinSlices), 0, s, a, b);
+    return hipGetLastError();
+}
+
+}  // namespace ddp

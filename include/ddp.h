@@ -1,6 +1,6 @@
 /* ddp.h — bucketed gradient reduction for data-parallel training, MI355X (gfx950):
- * the reduction, the norm and clipping of its results, the AdamW step, and the
- * embedding's lookup and gradient.
+ * the reduction, the norm and clipping of its results, the AdamW step, the
+ * embedding's lookup and gradient, and the layer norm's two passes.
  *
  * C ABI of libddp.so. Plain pointers and sizes only; every function returns
  * an int status (DDP_OK = 0, negative on error, text in ddp_last_error())
@@ -720,6 +720,81 @@ size_t ddp_embedding_grad_workspace_bytes(const ddp_embedding_desc *desc, int64_
  * workspace, and for one that overlaps another argument. */
 int ddp_embedding_grad(const ddp_embedding_desc *desc, const void *dout, const void *tokens, int64_t n_tokens,
                        void *grad, int32_t accumulate, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Layer norm: rows normalised, and the backward pass with the weight's gradient.
+ *
+ * The norms' weights are the other parameters whose gradients are not matrix
+ * products but sums over all positions. ddp_layernorm_grad adds them straight
+ * to the parameters' places in the flat buffer, as ddp_embedding_grad does, or
+ * writes whole gradients for the reducer to read.
+ * ------------------------------------------------------------------------- */
+enum {
+    DDP_LAYER_NORM = 0,   /* by mean and variance                                                         */
+    DDP_RMS_NORM = 1      /* by the mean square: no mean is taken off                                     */
+};
+
+typedef struct {
+    int64_t width;          /* H, 0 <= H <= 2^26                                                     */
+    int64_t x_stride;       /* elements between two rows of x, and of dx; all strides in [0, 2^31]    */
+    int64_t add_stride;     /* of add (0: one row for every position)                                */
+    int64_t z_stride;       /* of z, and of dz                                                       */
+    int64_t y_stride;       /* of y, and of dy (dy: 0 is one row for every position)                 */
+    float eps;              /* added to the variance, finite and >= 0                                */
+    int32_t kind;           /* DDP_LAYER_NORM or DDP_RMS_NORM                                        */
+    int32_t x_dtype;        /* of x, add, z, dz and dx: DDP_F32, DDP_BF16 or DDP_F16                 */
+    int32_t y_dtype;        /* of y and dy: x_dtype, or any if that is DDP_F32                       */
+    int32_t weight_dtype;   /* of weight and bias                                                    */
+    int32_t grad_dtype;     /* of dweight and dbias                                                  */
+} ddp_layernorm_desc;
+
+/* For each row of n_rows (in [0, 2^31)):
+ *   z    = R(x + add), or x where add is NULL
+ *   mean = sum z / H                        0 for DDP_RMS_NORM
+ *   rstd = 1 / sqrt(sum (z - mean)^2 / H + eps)
+ *   y    = R((z - mean) * rstd * weight + bias)
+ * in fp32 from the rounded z, R one rounding to the element's type. weight and
+ * bias [H] may be NULL (1 and 0). z is written where it is given (with add
+ * only), mean and rstd [n_rows] where they are: what the backward pass needs.
+ * All pointers are device memory at multiples of their element's size. Outputs
+ * must overlap no argument, except that z and y may each lie exactly where x
+ * or add does (same address, stride and element size). Rows of two arguments
+ * may interleave if their strides are equal. Elements between the rows are
+ * left alone. May be recorded into a HIP graph.
+ * Errors: DDP_ERR_INVALID (bad desc or row count, NULL, misaligned or
+ * overlapping arguments, a stride of x, z or y below the width, a stream of
+ * another device than the current one), DDP_ERR_HIP. */
+int ddp_layernorm(const ddp_layernorm_desc *desc, int64_t n_rows, const void *x, const void *add, const void *weight,
+                  const void *bias, void *z, void *y, float *mean, float *rstd, void *stream);
+
+/* Device workspace of one ddp_layernorm_grad call of up to n_rows rows: partial
+ * sums, at most 512 times dweight and dbias in fp32. Returns 0 and sets
+ * ddp_last_error() if the desc is invalid. */
+size_t ddp_layernorm_grad_workspace_bytes(const ddp_layernorm_desc *desc, int64_t n_rows);
+
+/* The backward pass, from the rows z that were normalised (x, or z where the
+ * forward pass had an add; rows z_stride apart) and their mean and rstd. With
+ * hat = (z - mean) * rstd and d = dy * weight:
+ *   dx      = R(rstd * (d - sum d / H - hat * sum(d * hat) / H) + dz)
+ *   dweight (+)= sum over the rows of dy * hat
+ *   dbias   (+)= sum over the rows of dy
+ * where DDP_RMS_NORM has no sum d / H (and does not look at mean). dz, the
+ * gradient that reaches z by another way, may be NULL (0), as may weight (1).
+ * dx is the gradient of x, and of add. A NULL dx, dweight or dbias is not
+ * computed. With accumulate != 0 dweight and dbias are added to what they
+ * hold; otherwise their old contents are not read. Everything is fp32, rounded
+ * once; the order of the additions depends on the sizes alone: the same call
+ * gives the same bits every time (no floating-point atomics).
+ * Pointers as for ddp_layernorm (workspace: 256 bytes; it may be NULL without
+ * dweight and dbias). Outputs and workspace must overlap no argument, except
+ * that dx may lie exactly where dy or dz does. A workspace serves one call at
+ * a time: calls that may run at once, replays of captured ones included, need
+ * one each. May be recorded into a HIP graph.
+ * Errors: as ddp_layernorm; DDP_ERR_INVALID for a missing or too small
+ * workspace. */
+int ddp_layernorm_grad(const ddp_layernorm_desc *desc, int64_t n_rows, const void *dy, const void *z, const void *dz,
+                       const void *weight, const float *mean, const float *rstd, void *dx, void *dweight, void *dbias,
+                       int32_t accumulate, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Text of the last error on this thread ("" if none). Never NULL. Where the
  * pages give PyTorch's wording of a Reducer error, the text starts with it
