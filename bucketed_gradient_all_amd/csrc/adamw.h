@@ -10,7 +10,7 @@ namespace ddp {
 
 // Elements of one tile: a workgroup of 256 threads takes it in two groups of
 // four elements a thread.
-constexpr int kAdamTile = 2048;
+constexpr int kAdamTile = 1024;
 
 // Elements of the 8-bit states that share a scale.
 constexpr int kStateBlock = 128;
