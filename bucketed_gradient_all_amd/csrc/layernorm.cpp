@@ -26,6 +26,9 @@ int64_t ceil_div(int64_t a, int64_t b)
     return (a + b - 1) / b;
 }
 
+// Bytes of z from which rows are read past the caches.
+constexpr int64_t kStreamBytes = int64_t(64) << 20;
+
 int element_size(int32_t type)
 {
     return type == DDP_F32 ? 4 : 2;
@@ -54,6 +57,12 @@ int check_desc(const ddp_layernorm_desc *d, int64_t n_rows)
     return DDP_OK;
 }
 
+// Whether rows are read past the caches.
+bool streams(const ddp_layernorm_desc &d, int64_t n_rows)
+{
+    return n_rows > kStreamBytes / (std::max<int64_t>(1, d.width) * element_size(d.x_dtype));
+}
+
 LayerArgs args_of(const ddp_layernorm_desc &d, int64_t n_rows)
 {
     LayerArgs a{};
@@ -65,6 +74,7 @@ LayerArgs args_of(const ddp_layernorm_desc &d, int64_t n_rows)
     a.y_stride = d.y_stride;
     a.eps = d.eps;
     a.rms = d.kind == DDP_RMS_NORM;
+    a.stream = streams(d, n_rows);
     a.x_dtype = d.x_dtype;
     a.y_dtype = d.y_dtype;
     a.weight_dtype = d.weight_dtype;
@@ -183,8 +193,8 @@ struct Plan {
     size_t bytes;      // of the workspace
 };
 
-// Parts at most: two workgroups a CU.
-constexpr int64_t kMostParts = 512;
+// Parts at most: eight waves a CU.
+constexpr int64_t kMostThreads = int64_t(512) * 256;
 
 Plan plan_of(const ddp_layernorm_desc &d, int64_t n_rows)
 {
@@ -192,9 +202,10 @@ Plan plan_of(const ddp_layernorm_desc &d, int64_t n_rows)
     const int64_t vec = ddp::layer_vector(d.x_dtype, d.y_dtype);
     const int64_t vectors = std::max<int64_t>(1, ceil_div(d.width, vec));
     p.wide = vectors > ddp::kRowVectors;
-    const int64_t at_once = p.wide || vectors <= 128 ? 4 : 1;   // rows of a workgroup
-    const int64_t most = p.wide ? std::max<int64_t>(1, 2 * kMostParts / ceil_div(vectors, 64)) : kMostParts;
-    p.n_parts = int32_t(std::min(most, ceil_div(n_rows, at_once)));
+    const ddp::RowPlan r = ddp::row_plan(vectors, streams(d, n_rows));
+    int64_t most = kMostThreads / r.threads, rows = r.rows;
+    if (p.wide) most = std::max<int64_t>(1, 1024 / ceil_div(vectors, 64)), rows = 4;
+    p.n_parts = int32_t(std::min(most, ceil_div(n_rows, rows)));
     p.bytes = (size_t(p.n_parts) * 2 * size_t(d.width) * sizeof(float) + kAlign - 1) / kAlign * kAlign + kAlign;
     return p;
 }

@@ -12,7 +12,8 @@ struct LayerArgs {
     int64_t rows, width;
     int64_t x_stride, add_stride, z_stride, y_stride;
     float eps;
-    int32_t rms;   // no mean is taken off
+    int32_t rms;      // no mean is taken off
+    int32_t stream;   // the rows are read past the caches
     int32_t x_dtype, y_dtype, weight_dtype, grad_dtype;
 };
 
@@ -25,6 +26,21 @@ constexpr int layer_vector(int x_dtype, int y_dtype)
 // Vectors of a row that is held in registers, at most: two in each thread of a
 // workgroup of 1024. Wider rows are read again for each pass over them.
 constexpr int kRowVectors = 2048;
+
+// The backward pass's workgroups, by the vectors of a row and whether rows are
+// read past the caches: threads, and rows taken at once.
+struct RowPlan {
+    int threads, rows;
+};
+constexpr RowPlan row_plan(int64_t vectors, bool stream)
+{
+    if (vectors > 512) return {512, 1};
+    if (vectors > 256) return {512, 2};
+    int shared = 8;   // threads of a row
+    while (shared < vectors) shared *= 2;
+    const int threads = stream ? 256 : 512;
+    return {threads, threads / shared * 2};
+}
 
 struct LayerForward {
     const void *x, *add;   // add: or NULL

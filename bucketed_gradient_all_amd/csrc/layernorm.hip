@@ -18,14 +18,14 @@ namespace ddp {
 namespace {
 
 // z's columns from x's and add's.
-template <int X, int VEC>
+template <int X, int VEC, bool STREAM = false>
 __device__ __forceinline__ void load_z(const LayerForward &f, const void *x, const void *add, const Columns<VEC> &c,
                                        float (&v)[VEC])
 {
-    widen_all<X, VEC>(load<X, VEC>(x, c.col), v);
+    widen_all<X, VEC>(load<X, VEC, STREAM>(x, c.col), v);
     if (f.add) {
         float w[VEC];
-        widen_all<X, VEC>(load<X, VEC>(add, c.col), w);
+        widen_all<X, VEC>(load<X, VEC, STREAM>(add, c.col), w);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) v[j] = widen<X>(narrow<X>(v[j] + w[j]));
     }
@@ -44,18 +44,30 @@ struct Stats {
     }
 };
 
+// Threads of a workgroup whose rows are shared by T threads each: 256, or T.
+constexpr int threads_of(int t)
+{
+    return t <= 64 ? 256 : t;
+}
+
 // A row in the registers of T threads, U vectors each.
 template <int X, int Y, int T, int U, int VEC>
 __global__ void __launch_bounds__(threads_of(T)) layernorm_rows(LayerArgs a, LayerForward f, int64_t first)
 {
-    const int group = T == 64 ? __builtin_amdgcn_readfirstlane(int(threadIdx.x) / 64) : 0;
-    const int64_t row = first + int64_t(blockIdx.x) * (threads_of(T) / T) + group;
-    if (row >= a.rows) return;   // whole waves, and no workgroup that shares a row
+    constexpr int THREADS = threads_of(T);
+    const int64_t row = first + int64_t(blockIdx.x) * (THREADS / T) + group_of<T>();
+    if (row >= a.rows) return;   // no thread of another row waits for these
     const int t = int(threadIdx.x) % T;
     const void *x = row_of<X>(f.x, row, a.x_stride), *add = row_of<X>(f.add, row, a.add_stride);
     float v[U][VEC];
 #pragma unroll
-    for (int u = 0; u < U; ++u) load_z<X, VEC>(f, x, add, Columns<VEC>(u * T + t, a.width), v[u]);
+    for (int u = 0; u < U; ++u) {
+        const Columns<VEC> c(u * T + t, a.width);
+        if (a.stream)
+            load_z<X, VEC, true>(f, x, add, c, v[u]);
+        else
+            load_z<X, VEC>(f, x, add, c, v[u]);
+    }
     if (f.z) {
         void *z = row_of<X>(f.z, row, a.z_stride);
 #pragma unroll
@@ -74,7 +86,7 @@ __global__ void __launch_bounds__(threads_of(T)) layernorm_rows(LayerArgs a, Lay
 #pragma unroll
             for (int j = 0; j < VEC; ++j) s[0] += j >= c.skip ? v[u][j] : 0.0f;
         }
-        row_sum<T>(s, turn);
+        row_sum<T, THREADS>(s, turn);
         mean = s[0] / float(a.width);
     }
     float s[2] = {0.0f, 0.0f};
@@ -88,7 +100,7 @@ __global__ void __launch_bounds__(threads_of(T)) layernorm_rows(LayerArgs a, Lay
             s[1] = __fmaf_rn(v[u][j], v[u][j], s[1]);
         }
     }
-    row_sum<T>(s, turn);
+    row_sum<T, THREADS>(s, turn);
     const Stats k(s[0], s[1], a);
     if (t == 0) {
         if (f.mean) ((GLOBAL float *)f.mean)[row] = mean + k.shift;
@@ -113,7 +125,7 @@ __global__ void __launch_bounds__(threads_of(T)) layernorm_rows(LayerArgs a, Lay
 template <int X, int Y, int VEC>
 __global__ void __launch_bounds__(1024) layernorm_wide(LayerArgs a, LayerForward f, int64_t first)
 {
-    constexpr int T = 1024;
+    constexpr int T = 1024, THREADS = T;
     const int64_t row = first + blockIdx.x;
     const void *x = row_of<X>(f.x, row, a.x_stride), *add = row_of<X>(f.add, row, a.add_stride);
     void *z = f.z ? row_of<X>(f.z, row, a.z_stride) : nullptr;
@@ -137,7 +149,7 @@ __global__ void __launch_bounds__(1024) layernorm_wide(LayerArgs a, LayerForward
             for (int j = 0; j < VEC; ++j) sum += j >= c.skip ? double(v[j]) : 0.0;
         }
         m[0] = float(sum);
-        row_sum<T>(m, turn);
+        row_sum<T, THREADS>(m, turn);
     }
     const float mean = a.rms ? 0.0f : m[0] / float(a.width);
     double sum = 0.0, squares = 0.0;
@@ -152,7 +164,7 @@ __global__ void __launch_bounds__(1024) layernorm_wide(LayerArgs a, LayerForward
         }
     }
     float s[2] = {float(sum), float(squares)};
-    row_sum<T>(s, turn);
+    row_sum<T, THREADS>(s, turn);
     const Stats k(s[0], s[1], a);
     if (threadIdx.x == 0) {
         if (f.mean) ((GLOBAL float *)f.mean)[row] = mean + k.shift;
@@ -193,17 +205,26 @@ hipError_t run_rows(const LayerArgs &a, const LayerForward &f, hipStream_t s)
 
 }  // namespace
 
+// A vector a thread, or two where that makes more waves than it saves: of 2^26
+// elements with weight and bias, 1024 16-bit columns take 92 us by one wave with
+// two vectors and 95 by two with one, 512 fp32 columns 186 and 173; 4096 16-bit
+// columns 143 us by one wave with eight, 101 by four with two, 100 by eight with
+// one; 8192 109 by four with four, 101 by eight with two, 110 by sixteen with one.
+// Narrow rows share a wave: 256 16-bit columns 91 us, 145 with a wave each.
 hipError_t launch_layernorm(const LayerArgs &a, const LayerForward &f, hipStream_t s)
 {
     return by_types(a, [&](auto x, auto y) {
         constexpr int X = x(), Y = y(), VEC = layer_vector(X, Y);
-        if (a.width < VEC) return run_rows<X, Y, 64, 1, 1>(a, f, s);
+        if (a.width < VEC) return run_rows<X, Y, 8, 1, 1>(a, f, s);
         const int64_t vectors = (a.width + VEC - 1) / VEC;
+        if (vectors <= 8) return run_rows<X, Y, 8, 1, VEC>(a, f, s);
+        if (vectors <= 16) return run_rows<X, Y, 16, 1, VEC>(a, f, s);
+        if (vectors <= 32) return run_rows<X, Y, 32, 1, VEC>(a, f, s);
         if (vectors <= 64) return run_rows<X, Y, 64, 1, VEC>(a, f, s);
-        if (vectors <= 128) return run_rows<X, Y, 64, 2, VEC>(a, f, s);
-        if (vectors <= 256) return run_rows<X, Y, 64, 4, VEC>(a, f, s);
-        if (vectors <= 512) return run_rows<X, Y, 64, 8, VEC>(a, f, s);
-        if (vectors <= 1024) return run_rows<X, Y, 256, 4, VEC>(a, f, s);
+        if (vectors <= 128) return run_rows<X, Y, VEC == 4 ? 128 : 64, VEC == 4 ? 1 : 2, VEC>(a, f, s);
+        if (vectors <= 256) return run_rows<X, Y, 256, 1, VEC>(a, f, s);
+        if (vectors <= 512) return run_rows<X, Y, 512, 1, VEC>(a, f, s);
+        if (vectors <= 1024) return run_rows<X, Y, 512, 2, VEC>(a, f, s);
         if (vectors <= kRowVectors) return run_rows<X, Y, 1024, 2, VEC>(a, f, s);
         return over_rows(a.rows, 1, [&](dim3 g, int64_t first) {
             hipLaunchKernelGGL((layernorm_wide<X, Y, VEC>), g, dim3(1024), 0, s, a, f, first);

@@ -40,90 +40,146 @@ struct Along {
 };
 
 template <int X, int VEC>
-__device__ __forceinline__ void store_dx(const LayerBackward &b, void *dx, const void *dz, const Columns<VEC> &c,
-                                         const float (&d)[VEC], const float (&hat)[VEC], const Along &k, float rstd)
+__device__ __forceinline__ void dx_of(const Along &k, float rstd, const float (&d)[VEC], const float (&hat)[VEC],
+                                      const typename Raw<X, VEC>::type &dz, float (&v)[VEC])
 {
-    float v[VEC];
+    widen_all<X, VEC>(dz, v);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) v[j] = (d[j] - k.shift - hat[j] * k.slope) * rstd;
-    if (b.dz) {
-        float w[VEC];
-        widen_all<X, VEC>(load<X, VEC>(dz, c.col), w);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) v[j] += w[j];
-    }
-    if (c.skip < VEC) store<X, VEC>(dx, c.col, v, c.skip);
+    for (int j = 0; j < VEC; ++j) v[j] = (d[j] - k.shift - hat[j] * k.slope) * rstd + v[j];
 }
 
-// Rows in the registers of T threads, U vectors each.
-template <int X, int Y, int T, int U, int VEC>
-__global__ void __launch_bounds__(threads_of(T)) layernorm_grad_rows(LayerArgs a, LayerBackward b)
+// Makes the compiler take a value for a new one: what was computed from it is
+// computed again, where it would otherwise fill registers until then.
+template <class V>
+__device__ __forceinline__ void forget(V &x)
 {
-    constexpr int GROUPS = threads_of(T) / T;
-    const int group = T == 64 ? __builtin_amdgcn_readfirstlane(int(threadIdx.x) / 64) : 0;
-    const int t = int(threadIdx.x) % T;
+    if constexpr (sizeof(V) >= 8) {
+        typedef uint32_t words __attribute__((ext_vector_type(sizeof(V) / 4)));
+        words w = __builtin_bit_cast(words, x);
+        asm volatile("" : "+v"(w));
+        x = __builtin_bit_cast(V, w);
+    }
+}
+
+// What R rows' backward pass reads, U vectors a thread.
+template <int X, int Y, int T, int U, int R, int VEC>
+struct Rows {
+    typename Raw<X, VEC>::type z[R][U], dz[R][U];
+    typename Raw<Y, VEC>::type dy[R][U];
+    float mean[R], rstd[R];
+
+    template <bool STREAM>
+    __device__ __forceinline__ void load_as(const LayerArgs &a, const LayerBackward &b, int64_t row0, int t)
+    {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t row = min(row0 + r, a.rows - 1);   // past the last row: the last again, not counted
+            mean[r] = b.mean ? ((const GLOBAL float *)b.mean)[row] : 0.0f;
+            rstd[r] = ((const GLOBAL float *)b.rstd)[row];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const Columns<VEC> c(u * T + t, a.width);
+                z[r][u] = load<X, VEC, STREAM>(row_of<X>(b.z, row, a.z_stride), c.col);
+                dy[r][u] = load<Y, VEC, STREAM>(row_of<Y>(b.dy, row, a.y_stride), c.col);
+                dz[r][u] = 0;
+                if (b.dz) dz[r][u] = load<X, VEC, STREAM>(row_of<X>(b.dz, row, a.z_stride), c.col);
+            }
+        }
+    }
+    __device__ __forceinline__ void load_rows(const LayerArgs &a, const LayerBackward &b, int64_t row0, int t)
+    {
+        if (a.stream)
+            load_as<true>(a, b, row0, t);
+        else
+            load_as<false>(a, b, row0, t);
+    }
+};
+
+// R rows at a time in the registers of T threads, U vectors of each: all their
+// loads are under way before the first is used, those of the next rows too with
+// AHEAD, and one barrier serves R rows. Between the sums and dx a row is kept as
+// it was read.
+template <int X, int Y, int THREADS, int T, int U, int R, bool AHEAD, int VEC>
+__global__ void __launch_bounds__(THREADS) layernorm_grad_rows(LayerArgs a, LayerBackward b)
+{
+    constexpr int GROUPS = THREADS / T;
+    const int group = group_of<T>(), t = int(threadIdx.x) % T;
     float w[U][VEC], dw[U][VEC] = {}, db[U][VEC] = {};
 #pragma unroll
     for (int u = 0; u < U; ++u)
         load_weight<VEC>(b.weight, a.weight_dtype, Columns<VEC>(u * T + t, a.width).col, 1.0f, w[u]);
     int turn = 0;
-    for (int64_t row = int64_t(blockIdx.x) * GROUPS + group; row < a.rows; row += int64_t(b.n_parts) * GROUPS) {
-        const void *z = row_of<X>(b.z, row, a.z_stride), *dy = row_of<Y>(b.dy, row, a.y_stride);
-        const float mean = b.mean ? ((const GLOBAL float *)b.mean)[row] : 0.0f;
-        const float rstd = ((const GLOBAL float *)b.rstd)[row];
-        typename Raw<X, VEC>::type zr[U];
-        typename Raw<Y, VEC>::type gr[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const Columns<VEC> c(u * T + t, a.width);
-            zr[u] = load<X, VEC>(z, c.col);
-            gr[u] = load<Y, VEC>(dy, c.col);
+    const int64_t step = int64_t(b.n_parts) * GROUPS * R;
+    Rows<X, Y, T, U, R, VEC> now, next;
+    if (AHEAD) next.load_rows(a, b, (int64_t(blockIdx.x) * GROUPS + group) * R, t);
+    // the same turns for all threads
+    for (int64_t first = int64_t(blockIdx.x) * GROUPS * R; first < a.rows; first += step) {
+        const int64_t row0 = first + group * R;
+        if (AHEAD) {
+            now = next;
+            if (first + step < a.rows) next.load_rows(a, b, row0 + step, t);
+        } else {
+            now.load_rows(a, b, row0, t);
         }
-        float s[2] = {0.0f, 0.0f};
-        float hat[U][VEC], d[U][VEC];
+        auto &[z, dz, dy, mean, rstd] = now;
+        float s[2 * R];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const Columns<VEC> c(u * T + t, a.width);
-            normalise<X, Y, VEC>(zr[u], gr[u], mean, rstd, c.skip, hat[u], d[u]);
+        for (int r = 0; r < R; ++r) {
+            s[2 * r] = s[2 * r + 1] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                dw[u][j] = __fmaf_rn(d[u][j], hat[u][j], dw[u][j]);
-                db[u][j] += d[u][j];
-                d[u][j] *= w[u][j];
-                s[0] += d[u][j];
-                s[1] = __fmaf_rn(d[u][j], hat[u][j], s[1]);
+            for (int u = 0; u < U; ++u) {
+                const Columns<VEC> c(u * T + t, a.width);
+                float hat[VEC], g[VEC];
+                normalise<X, Y, VEC>(z[r][u], dy[r][u], mean[r], rstd[r], row0 + r < a.rows ? c.skip : VEC, hat, g);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    dw[u][j] = __fmaf_rn(g[j], hat[j], dw[u][j]);
+                    db[u][j] += g[j];
+                    const float d = g[j] * w[u][j];
+                    s[2 * r] += d;
+                    s[2 * r + 1] = __fmaf_rn(d, hat[j], s[2 * r + 1]);
+                }
             }
         }
         if (!b.dx) continue;
-        row_sum<T>(s, turn);
-        const Along k(s[0], s[1], a);
-        void *dx = row_of<X>(b.dx, row, a.x_stride);
-        const void *dz = row_of<X>(b.dz, row, a.z_stride);
+        row_sum<T, THREADS>(s, turn);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            store_dx<X, VEC>(b, dx, dz, Columns<VEC>(u * T + t, a.width), d[u], hat[u], k, rstd);
+        for (int r = 0; r < R; ++r) {
+            if (row0 + r >= a.rows) continue;
+            const Along k(s[2 * r], s[2 * r + 1], a);
+            void *dx = row_of<X>(b.dx, row0 + r, a.x_stride);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const Columns<VEC> c(u * T + t, a.width);
+                float hat[VEC], d[VEC], v[VEC];
+                forget(z[r][u]);
+                forget(dy[r][u]);
+                normalise<X, Y, VEC>(z[r][u], dy[r][u], mean[r], rstd[r], c.skip, hat, d);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) d[j] *= w[u][j];
+                dx_of<X, VEC>(k, rstd[r], d, hat, dz[r][u], v);
+                if (c.skip < VEC) store<X, VEC>(dx, c.col, v, c.skip);
+            }
+        }
     }
     if (!b.parts) return;
     float *part = b.parts + int64_t(blockIdx.x) * 2 * a.width;
     if constexpr (GROUPS > 1) {
         // the groups' sums, added in order
-        __shared__ float sums[2][GROUPS][64][VEC];
+        __shared__ float sums[2][GROUPS][T * VEC];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (u > 0) __syncthreads();
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) sums[0][group][t][j] = dw[u][j], sums[1][group][t][j] = db[u][j];
+            for (int j = 0; j < VEC; ++j) sums[0][group][t * VEC + j] = dw[u][j], sums[1][group][t * VEC + j] = db[u][j];
             __syncthreads();
-            const Columns<VEC> c(u * T + t, a.width);
-            if (group < 2) {
-                float v[VEC];
+            for (int i = int(threadIdx.x); i < 2 * T * VEC; i += THREADS) {
+                const int which = i / (T * VEC), at = i % (T * VEC);
+                const Columns<VEC> c(u * T + at / VEC, a.width);
+                float v = sums[which][0][at];
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    v[j] = sums[group][0][t][j];
-#pragma unroll
-                    for (int k = 1; k < GROUPS; ++k) v[j] += sums[group][k][t][j];
-                }
-                if (c.skip < VEC) store<DDP_F32, VEC>(part + group * a.width, c.col, v, c.skip);
+                for (int k = 1; k < GROUPS; ++k) v += sums[which][k][at];
+                if (at % VEC >= c.skip) ((GLOBAL float *)part)[which * a.width + c.col + at % VEC] = v;
             }
         }
     } else {
@@ -146,7 +202,6 @@ __global__ void __launch_bounds__(1024) layernorm_grad_wide(LayerArgs a, LayerBa
     constexpr int T = 1024;
     const int64_t row = first + blockIdx.x;
     const void *z = row_of<X>(b.z, row, a.z_stride), *dy = row_of<Y>(b.dy, row, a.y_stride);
-    const void *dz = row_of<X>(b.dz, row, a.z_stride);
     void *dx = row_of<X>(b.dx, row, a.x_stride);
     const float mean = b.mean ? ((const GLOBAL float *)b.mean)[row] : 0.0f;
     const float rstd = ((const GLOBAL float *)b.rstd)[row];
@@ -170,12 +225,16 @@ __global__ void __launch_bounds__(1024) layernorm_grad_wide(LayerArgs a, LayerBa
     }
     float s[2] = {float(sum), float(along)};
     int turn = 0;
-    row_sum<T>(s, turn);
+    row_sum<T, T>(s, turn);
     const Along k(s[0], s[1], a);
     for (int64_t i = threadIdx.x; i < vectors; i += T) {
         const Columns<VEC> c(i, a.width);
         take(c);
-        store_dx<X, VEC>(b, dx, dz, c, d, hat, k, rstd);
+        typename Raw<X, VEC>::type dz = 0;
+        if (b.dz) dz = load<X, VEC>(row_of<X>(b.dz, row, a.z_stride), c.col);
+        float v[VEC];
+        dx_of<X, VEC>(k, rstd, d, hat, dz, v);
+        store<X, VEC>(dx, c.col, v, c.skip);
     }
 }
 
@@ -252,11 +311,21 @@ __global__ void __launch_bounds__(kJoinColumns *kJoinSlices) layernorm_grad_join
         put(std::integral_constant<int, DDP_F16>());
 }
 
-template <int X, int Y, int T, int U, int VEC>
+template <int X, int Y, int THREADS, int T, int U, int R, bool AHEAD, int VEC>
 hipError_t run_grad(const LayerArgs &a, const LayerBackward &b, hipStream_t s)
 {
-    hipLaunchKernelGGL((layernorm_grad_rows<X, Y, T, U, VEC>), dim3(b.n_parts), dim3(threads_of(T)), 0, s, a, b);
+    static_assert(row_plan(T * U, THREADS == 256).threads == THREADS && row_plan(T * U, THREADS == 256).rows == THREADS / T * R,
+                  "the parts are planned for it");
+    hipLaunchKernelGGL((layernorm_grad_rows<X, Y, THREADS, T, U, R, AHEAD, VEC>), dim3(b.n_parts), dim3(THREADS), 0, s,
+                       a, b);
     return hipGetLastError();
+}
+
+// Rows of up to 256 vectors, a vector a thread.
+template <int X, int Y, int T, int VEC>
+hipError_t run_narrow(const LayerArgs &a, const LayerBackward &b, hipStream_t s)
+{
+    return a.stream ? run_grad<X, Y, 256, T, 1, 2, true, VEC>(a, b, s) : run_grad<X, Y, 512, T, 1, 2, true, VEC>(a, b, s);
 }
 
 }  // namespace
@@ -265,14 +334,17 @@ hipError_t launch_layernorm_rows(const LayerArgs &a, const LayerBackward &b, hip
 {
     return by_types(a, [&](auto x, auto y) {
         constexpr int X = x(), Y = y(), VEC = layer_vector(X, Y);
-        if (a.width < VEC) return run_grad<X, Y, 64, 1, 1>(a, b, s);
+        if (a.width < VEC) return run_narrow<X, Y, 8, 1>(a, b, s);
         const int64_t vectors = (a.width + VEC - 1) / VEC;
-        if (vectors <= 64) return run_grad<X, Y, 64, 1, VEC>(a, b, s);
-        if (vectors <= 128) return run_grad<X, Y, 64, 2, VEC>(a, b, s);
-        if (vectors <= 256) return run_grad<X, Y, 256, 1, VEC>(a, b, s);
-        if (vectors <= 512) return run_grad<X, Y, 256, 2, VEC>(a, b, s);
-        if (vectors <= 1024) return run_grad<X, Y, 512, 2, VEC>(a, b, s);
-        return run_grad<X, Y, 1024, 2, VEC>(a, b, s);
+        if (vectors <= 8) return run_narrow<X, Y, 8, VEC>(a, b, s);
+        if (vectors <= 16) return run_narrow<X, Y, 16, VEC>(a, b, s);
+        if (vectors <= 32) return run_narrow<X, Y, 32, VEC>(a, b, s);
+        if (vectors <= 64) return run_narrow<X, Y, 64, VEC>(a, b, s);
+        if (vectors <= 128) return run_narrow<X, Y, 128, VEC>(a, b, s);
+        if (vectors <= 256) return run_narrow<X, Y, 256, VEC>(a, b, s);
+        if (vectors <= 512) return run_grad<X, Y, 512, 256, 2, 1, true, VEC>(a, b, s);
+        if (vectors <= 1024) return run_grad<X, Y, 512, 512, 2, 1, true, VEC>(a, b, s);
+        return run_grad<X, Y, 512, 512, 4, 1, false, VEC>(a, b, s);
     });
 }
 

@@ -29,10 +29,15 @@ struct Columns {
     }
 };
 
-template <int TYPE, int VEC>
+// STREAM: past the caches.
+template <int TYPE, int VEC, bool STREAM = false>
 __device__ __forceinline__ typename Raw<TYPE, VEC>::type load(const void *base, int64_t e)
 {
-    return *(const GLOBAL typename Raw<TYPE, VEC>::any *)(static_cast<const typename Raw<TYPE, VEC>::elem *>(base) + e);
+    const auto p = (const GLOBAL typename Raw<TYPE, VEC>::any *)(static_cast<const typename Raw<TYPE, VEC>::elem *>(base) + e);
+    if constexpr (STREAM)
+        return __builtin_nontemporal_load(p);
+    else
+        return *p;
 }
 
 template <int TYPE>
@@ -63,7 +68,7 @@ __device__ __forceinline__ void store(void *base, int64_t e, const float (&v)[VE
 #pragma unroll
     for (int j = 0; j < VEC; ++j) x[j] = narrow<TYPE>(v[j]);
     if (skip == 0) {
-        *(GLOBAL typename R::any *)p = x;
+        __builtin_nontemporal_store(x, (GLOBAL typename R::any *)p);
     } else {
 #pragma unroll
         for (int j = 0; j < VEC; ++j)
@@ -93,36 +98,46 @@ __device__ __forceinline__ float with_lane(float x)
     return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CONTROL, 0xf, 0xf, false));
 }
 
-// The sum of a wave's values, the same bits in every lane.
-__device__ __forceinline__ float wave_sum(float x)
+// The sum of T neighbouring lanes' values, the same bits in each of them.
+template <int T>
+__device__ __forceinline__ float lane_sum(float x)
 {
     x = with_lane<0xb1>(x);    // the neighbour
     x = with_lane<0x4e>(x);    // the other pair of four
     x = with_lane<0x141>(x);   // the other four of eight
-    x = with_lane<0x140>(x);   // the other eight of sixteen
-    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+    if (T >= 16) x = with_lane<0x140>(x);   // the other eight of sixteen
+    if (T >= 32) {
+        const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    }
+    if (T >= 64) {
+        const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = __uint_as_float(b[0]) + __uint_as_float(b[1]);
+    }
+    return x;
 }
 
-// Threads of a workgroup whose rows are shared by T threads each.
-constexpr int threads_of(int t)
+// Which of the workgroup's rows a thread works on, where T threads share one.
+template <int T>
+__device__ __forceinline__ int group_of()
 {
-    return t < 256 ? 256 : t;
+    const int group = int(threadIdx.x) / T;
+    return T >= 64 ? __builtin_amdgcn_readfirstlane(group) : group;
 }
 
-// Sums over the T threads that share a row, the same bits in each of them: one
-// wave, or a whole workgroup. A workgroup's threads call it together; `turn`
-// counts the calls, so that one barrier a call is enough.
-template <int T, int N>
+// Sums over the T threads that share a row, the same bits in each of them: lanes
+// of a wave, or several waves of a workgroup of THREADS, whose threads call it
+// together then; `turn` counts the calls, so that one barrier a call is enough.
+template <int T, int THREADS, int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], int &turn)
 {
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = wave_sum(v[k]);
+    for (int k = 0; k < N; ++k) v[k] = lane_sum<T>(v[k]);
     if constexpr (T > 64) {
-        __shared__ float part[2][T / 64][N];
+        __shared__ float part[2][THREADS / 64][N];
+        constexpr int WAVES = T / 64;
         const int wave = int(threadIdx.x) / 64, slot = turn & 1;
+        const int first = THREADS == T ? 0 : wave / WAVES * WAVES;
         ++turn;
         if (threadIdx.x % 64 == 0) {
 #pragma unroll
@@ -131,9 +146,9 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int &turn)
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            v[k] = part[slot][0][k];
+            v[k] = part[slot][first][k];
 #pragma unroll
-            for (int w = 1; w < T / 64; ++w) v[k] += part[slot][w][k];
+            for (int w = 1; w < WAVES; ++w) v[k] += part[slot][first + w][k];
         }
     }
 }
