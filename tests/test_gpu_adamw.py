@@ -524,3 +524,29 @@ def test_a_flat_buffer_of_odd_views_equals_separate_tensors(bits):
     torch.cuda.synchronize()
     for a, b in zip(c.p + c.m + c.v, d.p + d.m + d.v):
         assert torch.equal(a, b)
+
+
+def test_more_elements_than_a_launch_holds():
+    """2^33 elements and some, in 16 bits with 8-bit states: the last ones step
+    as in a list of their own."""
+    torch, ddp = _torch(), _lib()
+    n, tail = (1 << 33) + 5000, 9000
+    c = Case([tail], grad=1, param=1, bits=8, seed=6, decay=0.1)
+    big = {k: torch.zeros(n, dtype=t, device="cuda") for k, t in
+           (("g", torch.bfloat16), ("p", torch.bfloat16), ("m", torch.uint8), ("v", torch.uint8))}
+    scales = [torch.zeros(blocks(n), device="cuda") for _ in range(2)]
+    lead = (n - tail) // BLOCK * BLOCK   # a block's border
+    k = tail // BLOCK * BLOCK
+    for name, t in (("g", c.g[0]), ("p", c.p[0]), ("m", c.m[0]), ("v", c.v[0])):
+        big[name][lead:lead + k] = t[:k]
+    for s, t in zip(scales, (c.ms[0], c.vs[0])):
+        s[lead // BLOCK:lead // BLOCK + k // BLOCK] = t[:k // BLOCK]
+    opt = ddp.make_adamw([n], [big["g"].data_ptr()], [big["p"].data_ptr()], [big["m"].data_ptr()], [big["v"].data_ptr()],
+                         grad_dtype=[1], param_dtype=[1], state=ddp.DDP_STATE_8BIT, m_scale_ptrs=[scales[0].data_ptr()],
+                         v_scale_ptrs=[scales[1].data_ptr()], weight_decay=0.1)
+    ddp.ddp_adamw_step(opt, 1e-3, 10, torch.cuda.current_stream().cuda_stream)
+    c.step(1e-3, 10)
+    torch.cuda.synchronize()
+    for name, t in (("p", c.p[0]), ("m", c.m[0]), ("v", c.v[0])):
+        assert torch.equal(big[name][lead:lead + k], t[:k]), name
+    assert not big["p"][:1 << 20].any() and not big["m"][lead - (1 << 20):lead].any()

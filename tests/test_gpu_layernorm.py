@@ -180,7 +180,7 @@ def test_forward_widths(kind, x, y):
 
 
 @pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 63, 257, 4099])
-@pytest.mark.parametrize("width", [6, 768, 1024, 2050])
+@pytest.mark.parametrize("width", [6, 40, 100, 200, 768, 1024, 2050])
 def test_forward_rows(rows, width):
     for kind, (x, y) in ((0, (1, 1)), (1, (0, 2))):
         f = Forward(rows, width, kind, x, y, weight=0, add="rows", seed=rows)
@@ -358,7 +358,7 @@ def test_backward_widths(kind, x, y):
 
 
 @pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 63, 511, 512, 513, 2049, 9001])
-@pytest.mark.parametrize("width", [6, 768, 1024, 2050])
+@pytest.mark.parametrize("width", [6, 40, 100, 200, 768, 1024, 2050])
 def test_backward_rows(rows, width):
     for kind, (x, y) in ((0, (1, 1)), (1, (0, 2))):
         b = Backward(rows, width, kind, x, y, seed=rows)
@@ -530,6 +530,45 @@ def test_special_streams():
         b.run(stream=stream)
         f.check()
         b.check()
+
+
+@pytest.mark.parametrize("rows,width,x,y", [(600001, 60, 1, 1), (140001, 250, 0, 0), (70001, 500, 1, 1), (33001, 1001, 0, 2),
+                                            (17001, 2047, 0, 1), (4201, 8100, 2, 2)])
+def test_large_inputs(rows, width, x, y):
+    """Rows that are read past the caches."""
+    for kind in (0, 1):
+        f = Forward(rows, width, kind, x, y, weight=x, add="rows", seed=1)
+        f.run()
+        f.check()
+        del f
+        b = Backward(rows, width, kind, x, y, weight=x, seed=2)
+        b.run()
+        b.check()
+        del b
+
+
+def test_more_rows_than_a_launch_holds():
+    torch, ddp = _torch(), _lib()
+    rows, width = (1 << 26) + 77, 8
+    x = torch.zeros(rows, width, dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros_like(x)
+    f = Forward(500, width, 0, 1, 1, seed=8)
+    x[:250] = f.x[:250]
+    x[-250:] = f.x[250:]
+    f.run()
+    ddp.ddp_layernorm(ddp.LayerNormDesc(width, x_dtype=1), rows, x.data_ptr(), ptr(f.weight), ptr(f.bias), y.data_ptr(), 0)
+    torch.cuda.synchronize()
+    assert torch.equal(y[:250], f.y[:250]) and torch.equal(y[-250:], f.y[250:])
+    assert (y[1000000:1000100] == f.bias.bfloat16()).all() and (y[-1000:-900] == f.bias.bfloat16()).all()
+
+
+def test_one_row_of_z_for_all():
+    b = Backward(40, 300, 0, 0, 0, dz=False)
+    b.z = b.z[:1].expand(40, -1)
+    b.desc.c.z_stride = 0
+    b.mean, b.rstd = b.mean[:1].expand(40).contiguous(), b.rstd[:1].expand(40).contiguous()
+    b.run()
+    b.check()
 
 
 def test_offsets_past_32_bits():
