@@ -1,6 +1,6 @@
 // One AdamW step over a list of tensors.
 //
-//   g = grad * f,  f = min(1, max_norm / (norm + 1e-6)), or 1 without a norm
+//   g = grad * f,  f = min(1, 1 / (norm + 1e-6) * max_norm), or 1 without a norm
 //   m = beta1 * m + (1 - beta1) * g
 //   v = beta2 * v + (1 - beta2) * g^2
 //   p = p * (1 - lr * decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
@@ -12,7 +12,7 @@
 // instructions an element, which the memory's time hides.
 //
 // 8-bit states: the m and r = sqrt(v) of a block of 128 elements are held as
-// e4m3 codes of m * (448 / max|m|), with max|m| / 448 as the block's scale.
+// e4m3 codes of m * (1 / max|m| * 448), with max|m| * (1 / 448) as the block's scale.
 //   * The root, because the codes' range of 2^-9 to 448 then spans 2^35 of v, and
 //     because the root is what the step divides by.
 //   * A positive r never gets the code of zero: with r = 0 beside an m that is
@@ -98,7 +98,7 @@ __device__ __forceinline__ bool scalars_of(const AdamArgs &a, double decay, Scal
         const float n = *(const CONSTANT float *)a.norm;
         if (a.skip && !(fabsf(n) < INFINITY)) return false;
         if (a.max_norm < INFINITY) {
-            const float f = __fdiv_rn(a.max_norm, __fadd_rn(n, 1e-6f));
+            const float f = __fmul_rn(__fdiv_rn(1.0f, __fadd_rn(n, 1e-6f)), a.max_norm);
             c->f = f >= 1.0f ? 1.0f : f;   // a NaN stays one
         }
     }
@@ -255,10 +255,8 @@ struct BlockScale {
     {
         const float top = __uint_as_float(top_bits);
         const bool none = top < 0x1p-100f;
-        constexpr float part = 1.0f / 448.0f;
-        const float d = top * part;
-        up = none ? 0.0f : quotient(448.0f, top);
-        down = none ? 0.0f : __fmaf_rn(__fmaf_rn(-448.0f, d, top), part, d);   // top / 448
+        up = none ? 0.0f : __fmul_rn(quotient(1.0f, top), 448.0f);
+        down = none ? 0.0f : __fmul_rn(top, 1.0f / 448.0f);
     }
 };
 

@@ -561,8 +561,9 @@ enum {
     DDP_STATE_F32 = 0,    /* both moments in fp32                                                         */
     DDP_STATE_8BIT = 1    /* both in 8 bits, with one fp32 scale for each DDP_STATE_BLOCK elements: the
                              first moment m, and the root r of the second, as e4m3 codes of
-                             m * (448 / max|m|) and r * (448 / max r) (round to nearest even; a positive r
-                             has at least the smallest positive code). m is code * scale, the second moment
+                             m * (1 / max|m| * 448) and r * (1 / max r * 448) (round to nearest even; a
+                             positive r has at least the smallest positive code). The scales are
+                             max|m| * (1 / 448) and max r * (1 / 448): m is code * scale, the second moment
                              (code * scale)^2. All codes and scales zero is the state before the first step.
                              A block whose max|m| is below 2^-100 is held as zeros; an infinity or a NaN
                              among a block's gradients leaves none of its states finite                   */
@@ -631,7 +632,7 @@ typedef struct {
 } ddp_adamw_args;
 
 /* One step of every tensor, on `stream`:
- *   g = grad * f,  f = min(1, max_norm / (norm + 1e-6)), or 1 without a norm
+ *   g = grad * f,  f = min(1, 1 / (norm + 1e-6) * max_norm), or 1 without a norm
  *   m = beta1 * m + (1 - beta1) * g
  *   v = beta2 * v + (1 - beta2) * g^2
  *   p = p * (1 - lr * weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)

@@ -69,7 +69,6 @@ def test_sizes_types_and_decays_are_checked(numel, kw, text):
 @pytest.mark.parametrize("make,kw,text", [
     (_desc, {"workspace": 0}, "workspace missing"),
     (_desc, {"workspace": WS + 8}, "workspace missing"),
-    (_desc, {"workspace_bytes": ddp.ddp_adamw_workspace_bytes(_desc()) - 1}, "workspace missing"),
     (_desc, {"grad_ptrs": [0]}, "tensor 0's gradient is NULL"),
     (_desc, {"param_ptrs": [0]}, "tensor 0's parameter is NULL"),
     (_desc, {"m_ptrs": [0]}, "tensor 0's m is NULL"),
@@ -93,6 +92,11 @@ def test_sizes_types_and_decays_are_checked(numel, kw, text):
 ])
 def test_pointers_are_checked(make, kw, text):
     _refused(lambda: ddp.ddp_adamw_create(make([64], **kw)), text)
+
+
+def test_a_workspace_that_is_too_small_is_refused():
+    need = ddp.ddp_adamw_workspace_bytes(_desc())
+    _refused(lambda: ddp.ddp_adamw_create(_desc(workspace_bytes=need - 1)), "workspace missing")
 
 
 @pytest.mark.parametrize("make,kw,text", [

@@ -88,7 +88,6 @@ def test_forward_pointers_are_checked(kw, text):
     ({"dbias": DB + 1}, "dbias is misaligned"), ({"weight": W + 2}, "weight is misaligned"),
     ({"rstd": RSTD + 2}, "rstd is misaligned"),
     ({"ws": 0}, "workspace missing"), ({"ws": WS + 64}, "workspace missing"),
-    ({"ws_bytes": ddp.ddp_layernorm_grad_workspace_bytes(ddp.LayerNormDesc(64), 4) - 1}, "workspace missing"),
     ({"dx": Z}, "dx and z overlap"), ({"dx": Y + 256}, "dx and dy overlap"), ({"dx": ADD + 4}, "dx and dz overlap"),
     ({"dweight": DB}, "overlap"), ({"dweight": W}, "dweight and weight overlap"), ({"dbias": DX + 64}, "overlap"),
     ({"dweight": MEAN}, "dweight and mean overlap"), ({"ws": Z}, "workspace and z overlap"),
@@ -96,6 +95,11 @@ def test_forward_pointers_are_checked(kw, text):
 ])
 def test_backward_pointers_are_checked(kw, text):
     _refused(lambda: _backward(_desc(), **kw), text)
+
+
+def test_a_workspace_that_is_too_small_is_refused():
+    need = ddp.ddp_layernorm_grad_workspace_bytes(_desc(), 4)
+    _refused(lambda: _backward(_desc(), ws_bytes=need - 1), "workspace missing")
 
 
 def test_strides_below_the_width_are_refused_for_outputs():
