@@ -101,16 +101,23 @@ struct Range {
     const char *what;
 };
 
+constexpr const char *kGrad = "gradient";   // the one range that is only read
+
+// Gradients may share memory; what is written meets nothing else.
 int check_overlap(std::vector<Range> &v)
 {
     std::sort(v.begin(), v.end(), [](const Range &a, const Range &b) { return a.lo < b.lo; });
     const auto name = [](const Range &r) { return r.of < 0 ? std::string(r.what) : tensor(r.of) + "'s " + r.what; };
-    for (size_t i = 1; i < v.size(); ++i)
-        if (v[i].lo < v[i - 1].hi) return fail(DDP_ERR_INVALID, name(v[i - 1]) + " and " + name(v[i]) + " overlap");
+    const Range *read = nullptr, *written = nullptr;   // that reach furthest so far
+    for (const Range &r : v) {
+        const bool reads = r.what == kGrad;
+        for (const Range *q : {written, reads ? nullptr : read})
+            if (q && r.lo < q->hi) return fail(DDP_ERR_INVALID, name(*q) + " and " + name(r) + " overlap");
+        const Range *&furthest = reads ? read : written;
+        if (!furthest || furthest->hi < r.hi) furthest = &r;
+    }
     return DDP_OK;
 }
-
-constexpr const char *kGrad = "gradient";   // the one range that a step does not write
 
 // Of the sorted ranges those that a step writes; touching ones become one.
 Spans written_of(const std::vector<Range> &v)

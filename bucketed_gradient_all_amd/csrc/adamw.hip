@@ -6,10 +6,13 @@
 //   p = p * (1 - lr * decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
 //   copy = R(p)                                  R: one rounding to the copy's type
 //
-// One pass over memory and no operand used twice, so it is bound by memory.
-// Everything is fp32 and every operation is rounded by itself (no product is
-// fused with a sum), with correctly rounded divisions and roots: about fifty
-// instructions an element, which the memory's time hides.
+// One pass over memory and no operand used twice, so it is bound by memory: 335M
+// fp32 parameters 1.55 ms (6.1 TB/s), 953M with bf16 gradients and a bf16 copy
+// 4.4 ms (6.1 TB/s), with 8-bit states 2.49 ms (6.2 TB/s). Everything is fp32 and
+// every operation is rounded by itself (no product is fused with a sum). With
+// 8-bit states an element takes nearly sixty instructions, two thirds of what the
+// memory's time leaves; the short quotient and root below are for them (with the
+// compiler's 2.58 ms).
 //
 // 8-bit states: the m and r = sqrt(v) of a block of 128 elements are held as
 // e4m3 codes of m * (1 / max|m| * 448), with max|m| * (1 / 448) as the block's scale.
@@ -103,10 +106,20 @@ __device__ __forceinline__ bool scalars_of(const AdamArgs &a, double decay, Scal
         }
     }
     if (a.lr_ptr || a.step_ptr) {
+        // one wave's 64-bit powers for the workgroup: 42M elements with 8-bit
+        // states 113 us, against 143 with all four waves' (and 87 to 100 with
+        // the host's scalars); 953M 2.51 ms against 2.72 and 2.50
+        __shared__ float found[2];
         if (a.lr_ptr) lr = double(*(const CONSTANT float *)a.lr_ptr);
-        const int64_t t = a.step_ptr ? max(int64_t(1), *(const CONSTANT int64_t *)a.step_ptr) : a.step;
-        c->size = float(lr / (1.0 - power(a.beta1, t)));
-        c->root = float(1.0 / __builtin_sqrt(1.0 - power(a.beta2, t)));
+        if (threadIdx.x < 64) {
+            const int64_t t = a.step_ptr ? max(int64_t(1), *(const CONSTANT int64_t *)a.step_ptr) : a.step;
+            const float size = float(lr / (1.0 - power(a.beta1, t)));
+            const float root = float(1.0 / __builtin_sqrt(1.0 - power(a.beta2, t)));
+            if (threadIdx.x == 0) found[0] = size, found[1] = root;
+        }
+        __syncthreads();
+        c->size = found[0];
+        c->root = found[1];
     }
     c->keep = float(1.0 - lr * decay);
     return true;
@@ -358,8 +371,11 @@ __global__ void __launch_bounds__(kThreads) adamw(AdamTables t, AdamArgs a, int 
 // Tiles of one launch: its grid holds 2^32 threads.
 constexpr int32_t kMostTiles = int32_t(1) << 23;
 
-// LDS that a workgroup of the 32-bit step reserves and does not use: four fit a
-// CU. Fewer streams at once suit the memory.
+// LDS that a workgroup of the 32-bit step reserves and does not use, so that four
+// fit a CU: fewer streams at once suit the memory. 335M elements take 1.52 ms
+// with four a CU, 1.58 with three, 1.57 with five, 1.62 with eight; 953M with a
+// copy 4.33, 4.40, 4.46 and 4.66. The 8-bit step has more to compute for each
+// byte and takes all eight (2.48 ms; four 3.17, six 2.59).
 constexpr unsigned kReserved = 40000;
 
 }  // namespace

@@ -26,7 +26,10 @@ int64_t ceil_div(int64_t a, int64_t b)
     return (a + b - 1) / b;
 }
 
-// Bytes of z from which rows are read past the caches.
+// Bytes of z from which rows are read past the caches; below, they may still lie
+// there from the kernel before. 128 MiB forward 85.5 us against 87.2, backward 97
+// against 100; 64 MiB forward 44.7 us against 45.6 from memory, but 44 against 40
+// where the caches hold a part.
 constexpr int64_t kStreamBytes = int64_t(64) << 20;
 
 int element_size(int32_t type)
@@ -50,10 +53,11 @@ int check_desc(const ddp_layernorm_desc *d, int64_t n_rows)
     if (d->x_dtype != DDP_F32 && d->y_dtype != d->x_dtype)
         return fail(DDP_ERR_INVALID, "y_dtype must be x_dtype unless that is DDP_F32");
     if (!(d->eps >= 0.0f) || std::isinf(d->eps)) return fail(DDP_ERR_INVALID, "eps must be finite and not negative");
-    // strides up to 2^31 keep every row's offset far inside 64 bits
     for (int64_t s : {d->x_stride, d->add_stride, d->z_stride, d->y_stride})
         if (s < 0 || s > (int64_t(1) << 31)) return fail(DDP_ERR_INVALID, "strides must be in [0, 2^31]");
     if (n_rows < 0 || n_rows >= (int64_t(1) << 31)) return fail(DDP_ERR_INVALID, "n_rows must be in [0, 2^31)");
+    if (std::max({d->x_stride, d->add_stride, d->z_stride, d->y_stride}) * n_rows > int64_t(1) << 58)
+        return fail(DDP_ERR_INVALID, "n_rows times a stride is too large");
     return DDP_OK;
 }
 

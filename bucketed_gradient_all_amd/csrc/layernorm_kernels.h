@@ -59,6 +59,9 @@ __device__ __forceinline__ void widen_all(const typename Raw<TYPE, VEC>::type &x
     for (int j = 0; j < VEC; ++j) v[j] = widen<TYPE>(x[j]);
 }
 
+// Written past the caches: 32768 rows of 2048 bf16 values forward 94 us against
+// 102, 16384 of 1024 fp32 values 54 against 58; with a kernel behind it that reads
+// y, 2048 rows of 2048 10.9 against 12.3, 8192 rows 36.8 against 34.4.
 template <int TYPE, int VEC>
 __device__ __forceinline__ void store(void *base, int64_t e, const float (&v)[VEC], int skip)
 {

@@ -608,8 +608,9 @@ size_t ddp_adamw_workspace_bytes(const ddp_adamw_desc *desc);
  * is used; not while a stream is being recorded; tied to the device that is
  * current here. *out is set only on success.
  * Errors: DDP_ERR_INVALID: bad sizes, types, decays or alignment; a copy
- * beside 16-bit parameters; any two of the tensors' ranges, or one and the
- * workspace, that overlap; DDP_ERR_HIP; DDP_ERR_NOMEM. */
+ * beside 16-bit parameters; a range that overlaps another of the tensors' or
+ * the workspace (gradients may share memory with each other: they are only
+ * read); DDP_ERR_HIP; DDP_ERR_NOMEM. */
 int ddp_adamw_create(const ddp_adamw_desc *desc, ddp_adamw **out);
 
 /* Releases the list's host state; touches no device memory. The workspace
@@ -619,7 +620,7 @@ int ddp_adamw_destroy(ddp_adamw *o);
 typedef struct {
     double lr;                /* finite, >= 0                                                       */
     double beta1, beta2;      /* in [0, 1)                                                          */
-    double eps;               /* finite, >= 0                                                       */
+    double eps;               /* finite, >= 0. With 0 an element without any gradient so far is 0 / 0 */
     int64_t step;             /* t, the number of this step, from 1 on                              */
     const float *lr_ptr;      /* device, one float that the step reads instead of lr; or NULL. With it
                                  and step_ptr the replays of a recorded step go on with the schedule */

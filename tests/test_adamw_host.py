@@ -117,7 +117,9 @@ def test_ranges_that_overlap_are_refused(make, kw, text):
 
 def test_tensors_that_share_memory_are_refused():
     _refused(lambda: ddp.ddp_adamw_create(_desc([64, 64], param_ptrs=[P, P])), "overlap")
-    _refused(lambda: ddp.ddp_adamw_create(_desc([64, 64], grad_ptrs=[G, G + 128])), "overlap")
+    _refused(lambda: ddp.ddp_adamw_create(_desc([64, 64], grad_ptrs=[G, G + 128], m_ptrs=[M, G + 380])), "overlap")
+    _refused(lambda: ddp.ddp_adamw_create(_desc([64, 64], grad_ptrs=[G, G], m_ptrs=[M, G])), "overlap")
+    _refused(lambda: ddp.ddp_adamw_create(_desc([6400, 64], grad_ptrs=[G, G + 64], m_ptrs=[M + 65536, G + 20000])), "overlap")
     _refused(lambda: ddp.ddp_adamw_create(_small([129, 64], m_scale_ptrs=[MS, MS + 4])), "overlap")
 
 

@@ -481,6 +481,21 @@ def test_lists_step_on_streams_of_their_own():
         assert all(torch.equal(a, b) for a, b in zip(c.contents(), g))
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_two_tensors_with_one_gradient(bits):
+    """Replicas' parameters that step from one reduced gradient."""
+    torch, ddp = _torch(), _lib()
+    c, d = (Case([5000], bits=bits, seed=3) for _ in range(2))
+    o = ddp.make_adamw(
+        [5000, 5000], [c.g[0].data_ptr()] * 2, [x.p[0].data_ptr() for x in (c, d)], [x.m[0].data_ptr() for x in (c, d)],
+        [x.v[0].data_ptr() for x in (c, d)], state=ddp.DDP_STATE_F32 if bits == 32 else ddp.DDP_STATE_8BIT,
+        m_scale_ptrs=[x.ms[0].data_ptr() for x in (c, d)] if bits == 8 else None,
+        v_scale_ptrs=[x.vs[0].data_ptr() for x in (c, d)] if bits == 8 else None, weight_decay=0.1)
+    ddp.ddp_adamw_step(o, 1e-3, 10, torch.cuda.current_stream().cuda_stream)
+    c.check(1e-3, 10)
+    assert all(torch.equal(a, b) for a, b in zip(c.contents(), d.contents()))
+
+
 def test_special_streams_and_an_empty_list():
     torch, ddp = _torch(), _lib()
     c = Case([4000], bits=32)

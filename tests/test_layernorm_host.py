@@ -68,6 +68,13 @@ def test_row_counts_are_checked(n):
     _refused(lambda: _backward(_desc(), n), "n_rows")
 
 
+def test_offsets_past_64_bits_are_refused():
+    for name in ("x_stride", "add_stride", "z_stride", "y_stride"):
+        d = _desc(**{name: 1 << 31})
+        _refused(lambda: _forward(d, (1 << 31) - 1), "too large")
+        _refused(lambda: _backward(d, (1 << 31) - 1), "too large")
+
+
 @pytest.mark.parametrize("kw,text", [
     ({"x": 0}, "x is NULL"), ({"y": 0}, "y is NULL"), ({"x": X + 2}, "x is misaligned"), ({"y": Y + 1}, "y is misaligned"),
     ({"add": ADD + 2}, "add is misaligned"), ({"z": Z + 2}, "z is misaligned"), ({"weight": W + 2}, "weight is misaligned"),
