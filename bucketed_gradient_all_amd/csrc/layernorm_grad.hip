@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(THREADS) layernorm_grad_rows(LayerArgs a, Laye
 #pragma unroll
             for (int j = 0; j < VEC; ++j) sums[0][group][t * VEC + j] = dw[u][j], sums[1][group][t * VEC + j] = db[u][j];
             __syncthreads();
-            for (int i = int(threadIdx.x); i < 2 * T * VEC; i += THREADS) {
+            for (int i = int(threadIdx.x); i < (b.dbias ? 2 : 1) * T * VEC; i += THREADS) {
                 const int which = i / (T * VEC), at = i % (T * VEC);
                 const Columns<VEC> c(u * T + at / VEC, a.width);
                 float v = sums[which][0][at];
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(THREADS) layernorm_grad_rows(LayerArgs a, Laye
             const Columns<VEC> c(u * T + t, a.width);
             if (c.skip < VEC) {
                 store<DDP_F32, VEC>(part, c.col, dw[u], c.skip);
-                store<DDP_F32, VEC>(part + a.width, c.col, db[u], c.skip);
+                if (b.dbias) store<DDP_F32, VEC>(part + a.width, c.col, db[u], c.skip);
             }
         }
     }
