@@ -155,7 +155,7 @@ int create(const ddp_adamw_desc *d, ddp_adamw **out)
     const bool small = d->state == DDP_STATE_8BIT;
     if (d->n_tensors > 0 && (!d->grads || !d->params || !d->m || !d->v))
         return fail(DDP_ERR_INVALID, "grads, params, m or v is NULL");
-    if (d->n_tensors > 0 && small != (d->m_scale && d->v_scale))
+    if (d->n_tensors > 0 && ((d->m_scale != nullptr) != small || (d->v_scale != nullptr) != small))
         return fail(DDP_ERR_INVALID, "m_scale and v_scale go with 8-bit states");
     const size_t need = table_bytes(*d);
     if (!d->workspace || d->workspace_bytes < need || reinterpret_cast<uintptr_t>(d->workspace) % kAlign)
@@ -256,8 +256,12 @@ bool bad_size(double x)
 int step(const ddp_adamw *o, const ddp_adamw_args *a, hipStream_t s)
 {
     if (!o || !a) return fail(DDP_ERR_INVALID, "NULL argument");
-    if ((!a->lr_ptr && bad_size(a->lr)) || bad_size(a->eps))
-        return fail(DDP_ERR_INVALID, "lr and eps must be finite and not negative");
+    if (!a->lr_ptr && bad_size(a->lr)) return fail(DDP_ERR_INVALID, "lr must be finite and not negative");
+    // the divisor of an element without a gradient: a subnormal one has no
+    // reciprocal in fp32
+    if (a->eps != 0.0 && !std::isnormal(float(a->eps)))
+        return fail(DDP_ERR_INVALID, "eps must be 0 or a normal fp32 number");
+    if (a->eps < 0.0) return fail(DDP_ERR_INVALID, "eps must not be negative");
     if (bad_rate(a->beta1) || bad_rate(a->beta2)) return fail(DDP_ERR_INVALID, "beta1 and beta2 must be in [0, 1)");
     if (!a->step_ptr && a->step < 1) return fail(DDP_ERR_INVALID, "step counts from 1");
     if (a->norm && !(a->max_norm >= 0.0f)) return fail(DDP_ERR_INVALID, "max_norm must not be negative");

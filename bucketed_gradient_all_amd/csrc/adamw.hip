@@ -162,7 +162,7 @@ __device__ __forceinline__ float update(const Scalars &c, float g, float &m, flo
     return r;
 }
 
-template <int GRAD, AdamOut OUT>
+template <AdamOut OUT>
 struct Types {
     static constexpr int param = OUT == kParamBF16 ? DDP_BF16 : OUT == kParamF16 ? DDP_F16 : DDP_F32;
     static constexpr int copy = OUT == kParamF32CopyBF16 ? DDP_BF16 : OUT == kParamF32CopyF16 ? DDP_F16 : -1;
@@ -171,7 +171,7 @@ struct Types {
 template <int GRAD, AdamOut OUT, bool FULL>
 __device__ __forceinline__ void step_32(const CONSTANT AdamSeg &s, int64_t base, const AdamArgs &a)
 {
-    typedef Types<GRAD, OUT> T;
+    typedef Types<OUT> T;
     const int64_t e = base + int(threadIdx.x) * kVec;
     const Some n = some_of<FULL>(e, s.len);
     const Vec<GRAD> g = load<GRAD>(s.grad, e, n);
@@ -261,7 +261,7 @@ __device__ __forceinline__ float of_pair(float x)
 
 // Of a block's largest magnitude: what its values are multiplied with before
 // they are rounded to codes, and the scale that undoes it. A block whose
-// largest is below 2^-100, whose 448 / top could overflow, is held as zeros.
+// largest is below 2^-100, where 1 / top * 448 could overflow, is held as zeros.
 struct BlockScale {
     float up, down;
     __device__ __forceinline__ explicit BlockScale(uint32_t top_bits)
@@ -283,7 +283,7 @@ static_assert(kStateBlock == 32 * kVec, "half a wave");
 template <int GRAD, AdamOut OUT, bool FULL>
 __device__ __forceinline__ void step_8(const CONSTANT AdamSeg &s, int64_t base, const AdamArgs &a)
 {
-    typedef Types<GRAD, OUT> T;
+    typedef Types<OUT> T;
     const int64_t e = base + int(threadIdx.x) * kVec;
     const Some n = some_of<FULL>(e, s.len);
     const int64_t block = e >> 7;

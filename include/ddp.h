@@ -588,8 +588,9 @@ typedef struct {
     const int32_t *copy_dtype;   /* [N] DDP_BF16 or DDP_F16 for each copy; given exactly with copies */
     void *const *m;              /* [N] first moments: fp32, or codes of one byte                   */
     void *const *v;              /* [N] second moments, the same                                    */
-    float *const *m_scale;       /* [N] 8-bit states: ceil(numel / DDP_STATE_BLOCK) scales, block b
-                                    that of the elements from b * DDP_STATE_BLOCK on; else not read */
+    float *const *m_scale;       /* [N] ceil(numel / DDP_STATE_BLOCK) scales, block b that of the
+                                    elements from b * DDP_STATE_BLOCK on; both arrays are given with
+                                    8-bit states, neither otherwise                                 */
     float *const *v_scale;
     const double *weight_decay;  /* [N] decay of each tensor, finite and >= 0; NULL: none           */
     void *workspace;             /* device memory of ddp_adamw_workspace_bytes() bytes, 16-byte
@@ -620,7 +621,8 @@ int ddp_adamw_destroy(ddp_adamw *o);
 typedef struct {
     double lr;                /* finite, >= 0                                                       */
     double beta1, beta2;      /* in [0, 1)                                                          */
-    double eps;               /* finite, >= 0. With 0 an element without any gradient so far is 0 / 0 */
+    double eps;               /* 0 or a normal, positive fp32 number. With 0 an element without any
+                                 gradient so far is 0 / 0                                            */
     int64_t step;             /* t, the number of this step, from 1 on                              */
     const float *lr_ptr;      /* device, one float that the step reads instead of lr; or NULL. With it
                                  and step_ptr the replays of a recorded step go on with the schedule */

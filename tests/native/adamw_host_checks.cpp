@@ -244,6 +244,8 @@ void steps()
         a = usual(), a.lr = bad, refused("lr", a);
         a = usual(), a.eps = bad, refused("eps", a);
     }
+    for (double bad : {1e-39, 1e-50, 1e39, -1e-50}) a = usual(), a.eps = bad, refused("eps beyond fp32's normal numbers", a);
+    for (double good : {0.0, 1e-37, 1e-8, 1.0}) a = usual(), a.eps = good, taken("eps", a);
     for (double bad : {-0.1, 1.0, 1.5, inf, nan}) {
         a = usual(), a.beta1 = bad, refused("beta1", a);
         a = usual(), a.beta2 = bad, refused("beta2", a);

@@ -85,6 +85,7 @@ def test_sizes_types_and_decays_are_checked(numel, kw, text):
     (_desc, {"copy_ptrs": [C], "copy_dtype": [1], "param_dtype": [1]}, "copy must be"),
     (_desc, {"m_ptrs": None}, "grads, params, m or v is NULL"),
     (_desc, {"m_scale_ptrs": [MS], "v_scale_ptrs": [VS]}, "go with 8-bit states"),
+    (_desc, {"v_scale_ptrs": [VS]}, "go with 8-bit states"),
     (_small, {"m_scale_ptrs": None}, "go with 8-bit states"),
     (_small, {"v_scale_ptrs": None}, "go with 8-bit states"),
     (_small, {"m_scale_ptrs": [0]}, "m_scale is NULL"),
