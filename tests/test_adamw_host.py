@@ -192,3 +192,37 @@ def test_host_source_under_sanitizers(tmp_path):
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=600, env=env)
     assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-4000:]
     assert "adamw_host_checks ok" in r.stdout
+
+
+class _Allocation:
+    device = "cuda:0"
+
+    def data_ptr(self):
+        return 0x100
+
+    def numel(self):
+        return 64
+
+
+@pytest.mark.parametrize("streams,waits", [((), False), ((0x7000,), False), ((0x7000, 0x9000), True), ((0,), True)])
+@pytest.mark.parametrize("destroy", [False, True])
+def test_tables_of_a_dropped_list_wait_for_other_streams(monkeypatch, streams, waits, destroy):
+    """As the gradient lists' do: memory used on its own stream alone is freed
+    at once, any other waits for the device."""
+    import gc
+    import types
+
+    import torch
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=0x7000))
+    monkeypatch.setattr(ddp, "_parked", [])
+    o, tables = ddp.AdamW(0), _Allocation()
+    o.own(tables)
+    for s in streams:
+        _refused(lambda: ddp.ddp_adamw_step(o, 1e-3, 1, s), "NULL argument")   # notes the stream first
+    if destroy:
+        ddp.ddp_adamw_destroy(o)
+        ddp.ddp_adamw_destroy(o)
+    else:
+        del o
+        gc.collect()
+    assert ddp._parked == ([tables] if waits else [])
