@@ -23,8 +23,8 @@ constexpr int layer_vector(int x_dtype, int y_dtype)
     return x_dtype == 0 || y_dtype == 0 ? 4 : 8;   // 0: DDP_F32
 }
 
-// Vectors of a row that is held in registers, at most: two in each thread of a
-// workgroup of 1024. Wider rows are read again for each pass over them.
+// Vectors of a row that the backward pass holds in registers, at most. Wider rows
+// are read again for each pass over them.
 constexpr int kRowVectors = 2048;
 
 // The backward pass's workgroups, by the vectors of a row and whether rows are

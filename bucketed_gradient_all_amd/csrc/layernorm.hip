@@ -212,6 +212,8 @@ hipError_t run_rows(const LayerArgs &a, const LayerForward &f, hipStream_t s)
 // two vectors and 95 by two with one, 512 fp32 columns 186 and 173; 4096 16-bit
 // columns 143 us by one wave with eight, 101 by four with two, 100 by eight with
 // one; 8192 109 by four with four, 101 by eight with two, 110 by sixteen with one.
+// Up to 32768 columns in registers: 16384 fp32 ones 215 us, 252 read again; 32768
+// 16-bit ones 118 and 139, but 20000 149 and 141.
 // Narrow rows share a wave: 256 16-bit columns 91 us, 145 with a wave each.
 hipError_t launch_layernorm(const LayerArgs &a, const LayerForward &f, hipStream_t s)
 {
@@ -227,7 +229,9 @@ hipError_t launch_layernorm(const LayerArgs &a, const LayerForward &f, hipStream
         if (vectors <= 256) return run_rows<X, Y, 256, 1, VEC>(a, f, s);
         if (vectors <= 512) return run_rows<X, Y, 512, 1, VEC>(a, f, s);
         if (vectors <= 1024) return run_rows<X, Y, 512, 2, VEC>(a, f, s);
-        if (vectors <= kRowVectors) return run_rows<X, Y, 1024, 2, VEC>(a, f, s);
+        if (vectors <= 2048) return run_rows<X, Y, 1024, 2, VEC>(a, f, s);
+        if (vectors <= 4096) return run_rows<X, Y, 1024, 4, VEC>(a, f, s);
+        if (VEC == 4 && vectors <= 8192) return run_rows<X, Y, 1024, VEC == 4 ? 8 : 4, VEC>(a, f, s);
         return over_rows(a.rows, 1, [&](dim3 g, int64_t first) {
             hipLaunchKernelGGL((layernorm_wide<X, Y, VEC>), g, dim3(1024), 0, s, a, f, first);
         });

@@ -36,7 +36,7 @@ D = P / 2 + 6
 HALF_SUBNORMAL = {0: 2.0 ** -150, 1: 2.0 ** -134, 2: 2.0 ** -25}
 PAIRS = [(0, 0), (0, 1), (0, 2), (1, 1), (2, 2)]   # x, y
 WIDTHS = [1, 2, 3, 4, 5, 7, 8, 9, 15, 16, 17, 63, 64, 65, 100, 127, 128, 255, 256, 257, 500, 511, 512, 513, 1000, 1023,
-          1024, 1025, 2047, 2048, 2049, 4095, 4096, 4097, 5000, 8191, 8192, 8193, 16383, 16384, 16385, 40001]
+          1024, 1025, 2047, 2048, 2049, 4095, 4096, 4097, 5000, 8191, 8192, 8193, 16383, 16384, 16385, 32767, 32768, 32769, 40001]
 
 
 def _torch():
@@ -199,7 +199,7 @@ def test_forward_arguments(affine, weight, add, z):
         f.check()
 
 
-@pytest.mark.parametrize("width", [64, 1000, 4096, 16390])
+@pytest.mark.parametrize("width", [64, 1000, 4096, 16390, 33000])
 @pytest.mark.parametrize("off", [0.0, 30.0, 1e4])
 def test_rows_far_off_centre(width, off):
     for rows_equal in (False, True):
@@ -222,7 +222,7 @@ def test_constant_and_zero_rows():
 
 
 @pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
-@pytest.mark.parametrize("width", [9, 1001, 20001])
+@pytest.mark.parametrize("width", [9, 1001, 20001, 33001])
 def test_values_that_are_not_finite_stay_in_their_row(bad, width):
     """Also in the columns that the last, overlapping vector loads twice."""
     torch = _torch()
@@ -237,7 +237,7 @@ def test_values_that_are_not_finite_stay_in_their_row(bad, width):
         assert torch.equal(f.y[others], clean.y[others]) and torch.equal(f.mean[others], clean.mean[others])
 
 
-@pytest.mark.parametrize("width", [5, 100, 2047, 4100, 16391])
+@pytest.mark.parametrize("width", [5, 100, 2047, 4100, 16391, 33001])
 @pytest.mark.parametrize("where", ["y is x", "z is x", "z is add", "z is x and y is add"])
 def test_forward_in_place(width, where):
     torch = _torch()
@@ -385,7 +385,7 @@ def test_backward_outputs_that_are_not_wanted(sums, dx, accumulate):
             b.check()
 
 
-@pytest.mark.parametrize("width", [5, 100, 2047, 4100, 16391])
+@pytest.mark.parametrize("width", [5, 100, 2047, 4100, 16391, 33001])
 @pytest.mark.parametrize("where", ["dy", "dz"])
 def test_backward_in_place(width, where):
     for kind in (0, 1):
@@ -416,7 +416,7 @@ def test_no_rows():
 
 
 @pytest.mark.parametrize("bad", [math.inf, math.nan])
-@pytest.mark.parametrize("width", [9, 1001, 20001])
+@pytest.mark.parametrize("width", [9, 1001, 20001, 33001])
 def test_gradients_that_are_not_finite_stay_in_row_and_column(bad, width):
     torch = _torch()
     for col in (0, width - 1, width - 2):
