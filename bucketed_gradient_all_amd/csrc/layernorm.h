@@ -65,7 +65,10 @@ struct LayerBackward {
 hipError_t launch_layernorm(const LayerArgs &a, const LayerForward &f, hipStream_t s);
 // dx and the parts; rows that fit the registers.
 hipError_t launch_layernorm_rows(const LayerArgs &a, const LayerBackward &b, hipStream_t s);
-// The same for rows of any width: dx alone, then the parts.
+// All of a small call: dx, dweight and dbias; rows that fit the registers, and
+// dx apart from dy.
+hipError_t launch_layernorm_small(const LayerArgs &a, const LayerBackward &b, hipStream_t s);
+// dx and the parts for rows of any width: the parts, then dx.
 hipError_t launch_layernorm_wide(const LayerArgs &a, const LayerBackward &b, hipStream_t s);
 // dweight and dbias from the parts.
 hipError_t launch_layernorm_join(const LayerArgs &a, const LayerBackward &b, hipStream_t s);

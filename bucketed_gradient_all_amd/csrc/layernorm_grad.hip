@@ -278,6 +278,22 @@ __global__ void __launch_bounds__(256) layernorm_grad_columns(LayerArgs a, Layer
     }
 }
 
+// One value of dweight or dbias, rounded once.
+__device__ __forceinline__ void put_gradient(const LayerArgs &a, const LayerBackward &b, void *out, int64_t col, float v)
+{
+    const auto put = [&](auto type) {
+        typedef Raw<decltype(type)::value, 1> R;
+        GLOBAL typename R::elem *p = (GLOBAL typename R::elem *)out + col;
+        *p = narrow<decltype(type)::value>(b.accumulate ? widen<decltype(type)::value>(*p) + v : v);
+    };
+    if (a.grad_dtype == DDP_F32)
+        put(std::integral_constant<int, DDP_F32>());
+    else if (a.grad_dtype == DDP_BF16)
+        put(std::integral_constant<int, DDP_BF16>());
+    else
+        put(std::integral_constant<int, DDP_F16>());
+}
+
 // Sums of the parts, 32 columns a workgroup, each column's parts dealt to 32
 // threads that add theirs in order, and then their sums.
 constexpr int kJoinColumns = 32, kJoinSlices = 32;
@@ -301,17 +317,128 @@ __global__ void __launch_bounds__(kJoinColumns *kJoinSlices) layernorm_grad_join
     s = sums[0][x];
 #pragma unroll
     for (int k = 1; k < kJoinSlices; ++k) s += sums[k][x];
-    const auto put = [&](auto type) {
-        typedef Raw<decltype(type)::value, 1> R;
-        GLOBAL typename R::elem *p = (GLOBAL typename R::elem *)out + col;
-        *p = narrow<decltype(type)::value>(b.accumulate ? widen<decltype(type)::value>(*p) + s : s);
-    };
-    if (a.grad_dtype == DDP_F32)
-        put(std::integral_constant<int, DDP_F32>());
-    else if (a.grad_dtype == DDP_BF16)
-        put(std::integral_constant<int, DDP_BF16>());
+    put_gradient(a, b, out, col, s);
+}
+
+// A small call in one launch: the first workgroups take the weight's and bias's
+// columns, the others the rows' dx. Both read z and dy, which the caches hold; it
+// spares the parts and the launch that adds them (when it pays is the host's
+// rule). dx may not lie where dy does.
+constexpr int kSmallThreads = 512;
+constexpr int kSlab = 4;   // vectors of columns of a workgroup: its threads go 128 rows at a time
+
+// The sum over a wave's lanes that are alike modulo 4, in its first four.
+__device__ __forceinline__ float over_slab(float x)
+{
+    x = with_lane<0x124>(x);   // four lanes on, of sixteen
+    x = with_lane<0x128>(x);   // eight on
+    return across_rows<64>(x);
+}
+
+// 32 columns' or so gradients over all rows, as the type that they have.
+template <int X, int Y, int VEC>
+__device__ __forceinline__ void small_columns(const LayerArgs &a, const LayerBackward &b)
+{
+    constexpr int GROUPS = kSmallThreads / kSlab, AHEAD = 4;
+    __shared__ float sums[kSmallThreads / 64][kSlab][2 * VEC];
+    const int lane = int(threadIdx.x) % kSlab, group = int(threadIdx.x) / kSlab;
+    const Columns<VEC> c(int64_t(blockIdx.x) * kSlab + lane, a.width);
+    float s[2 * VEC] = {};
+    for (int64_t first = group; first < a.rows; first += AHEAD * GROUPS) {
+        typename Raw<X, VEC>::type z[AHEAD];
+        typename Raw<Y, VEC>::type dy[AHEAD];
+        float mean[AHEAD], rstd[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int64_t row = min(first + k * GROUPS, a.rows - 1);   // past the last row: the last again, not counted
+            mean[k] = b.mean ? ((const GLOBAL float *)b.mean)[row] : 0.0f;
+            rstd[k] = ((const GLOBAL float *)b.rstd)[row];
+            z[k] = load<X, VEC>(row_of<X>(b.z, row, a.z_stride), c.col);
+            dy[k] = load<Y, VEC>(row_of<Y>(b.dy, row, a.y_stride), c.col);
+        }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            float hat[VEC], g[VEC];
+            normalise<X, Y, VEC>(z[k], dy[k], mean[k], rstd[k], first + k * GROUPS < a.rows ? c.skip : VEC, hat, g);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                s[j] = __fmaf_rn(g[j], hat[j], s[j]);
+                s[VEC + j] += g[j];
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 2 * VEC; ++j) {
+        s[j] = over_slab(s[j]);
+        if (threadIdx.x % 64 < kSlab) sums[threadIdx.x / 64][lane][j] = s[j];
+    }
+    __syncthreads();
+    const int i = int(threadIdx.x), which = i / (kSlab * VEC), at = i % (kSlab * VEC), j = at % VEC;
+    void *out = which ? b.dbias : b.dweight;
+    if (which > 1 || !out) return;
+    const Columns<VEC> o(int64_t(blockIdx.x) * kSlab + at / VEC, a.width);
+    if (j < o.skip) return;
+    float v = sums[0][at / VEC][which * VEC + j];
+#pragma unroll
+    for (int w = 1; w < kSmallThreads / 64; ++w) v += sums[w][at / VEC][which * VEC + j];
+    put_gradient(a, b, out, o.col + j, v);
+}
+
+// dx of rows in the registers of T threads, four vectors each.
+template <int X, int Y, int T, int VEC>
+__device__ __forceinline__ void small_rows(const LayerArgs &a, const LayerBackward &b, int block)
+{
+    constexpr int U = 4;
+    const int t = int(threadIdx.x) % T;
+    const int64_t row = int64_t(block) * (kSmallThreads / T) + group_of<T>();
+    if (row >= a.rows) return;   // no thread of another row waits for these
+    Rows<X, Y, T, U, 1, VEC> in;
+    in.template load_as<false>(a, b, row, t);
+    auto &[z, dz, dy, mean, rstd] = in;
+    float s[2] = {0.0f, 0.0f};
+    float hat[U][VEC], d[U][VEC];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const Columns<VEC> c(u * T + t, a.width);
+        float w[VEC];
+        load_weight<VEC>(b.weight, a.weight_dtype, c.col, 1.0f, w);
+        normalise<X, Y, VEC>(z[0][u], dy[0][u], mean[0], rstd[0], c.skip, hat[u], d[u]);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            d[u][j] *= w[j];
+            s[0] += d[u][j];
+            s[1] = __fmaf_rn(d[u][j], hat[u][j], s[1]);
+        }
+    }
+    int turn = 0;
+    row_sum<T, kSmallThreads>(s, turn);
+    const Along k(s[0], s[1], a);
+    void *dx = row_of<X>(b.dx, row, a.x_stride);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const Columns<VEC> c(u * T + t, a.width);
+        float v[VEC];
+        dx_of<X, VEC>(k, rstd[0], d[u], hat[u], dz[0][u], v);
+        if (c.skip < VEC) store<X, VEC>(dx, c.col, v, c.skip);
+    }
+}
+
+template <int X, int Y, int T, int VEC>
+__global__ void __launch_bounds__(kSmallThreads) layernorm_grad_small(LayerArgs a, LayerBackward b, int slabs)
+{
+    if (int(blockIdx.x) < slabs)
+        small_columns<X, Y, VEC>(a, b);
     else
-        put(std::integral_constant<int, DDP_F16>());
+        small_rows<X, Y, T, VEC>(a, b, int(blockIdx.x) - slabs);
+}
+
+template <int X, int Y, int T, int VEC>
+hipError_t run_small(const LayerArgs &a, const LayerBackward &b, hipStream_t s)
+{
+    const int64_t each = kSmallThreads / T, slabs = (a.width + kSlab * VEC - 1) / (kSlab * VEC);
+    const dim3 g(static_cast<unsigned>(slabs + (b.dx ? (a.rows + each - 1) / each : 0)));
+    hipLaunchKernelGGL((layernorm_grad_small<X, Y, T, VEC>), g, dim3(kSmallThreads), 0, s, a, b, int(slabs));
+    return hipGetLastError();
 }
 
 template <int X, int Y, int THREADS, int T, int U, int R, bool AHEAD, int VEC>
@@ -357,6 +484,16 @@ hipError_t launch_layernorm_rows(const LayerArgs &a, const LayerBackward &b, hip
         // 2^26 bf16 values in rows of 16384 131 us; by 1024 threads with two
         // vectors each, which leaves them half the registers, 165
         return run_grad<X, Y, 512, 512, 4, 1, false, VEC>(a, b, s);
+    });
+}
+
+hipError_t launch_layernorm_small(const LayerArgs &a, const LayerBackward &b, hipStream_t s)
+{
+    return by_types(a, [&](auto x, auto y) {
+        constexpr int X = x(), Y = y(), VEC = layer_vector(X, Y);
+        if (a.width < VEC) return run_small<X, Y, 64, 1>(a, b, s);
+        // a wave a row, or a workgroup
+        return a.width <= 256 * VEC ? run_small<X, Y, 64, VEC>(a, b, s) : run_small<X, Y, 512, VEC>(a, b, s);
     });
 }
 

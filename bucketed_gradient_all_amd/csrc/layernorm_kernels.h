@@ -101,14 +101,10 @@ __device__ __forceinline__ float with_lane(float x)
     return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CONTROL, 0xf, 0xf, false));
 }
 
-// The sum of T neighbouring lanes' values, the same bits in each of them.
+// The sum over the sixteens that T lanes are, lane by lane, in each of them.
 template <int T>
-__device__ __forceinline__ float lane_sum(float x)
+__device__ __forceinline__ float across_rows(float x)
 {
-    x = with_lane<0xb1>(x);    // the neighbour
-    x = with_lane<0x4e>(x);    // the other pair of four
-    x = with_lane<0x141>(x);   // the other four of eight
-    if (T >= 16) x = with_lane<0x140>(x);   // the other eight of sixteen
     if (T >= 32) {
         const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
         x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
@@ -118,6 +114,17 @@ __device__ __forceinline__ float lane_sum(float x)
         x = __uint_as_float(b[0]) + __uint_as_float(b[1]);
     }
     return x;
+}
+
+// The sum of T neighbouring lanes' values, the same bits in each of them.
+template <int T>
+__device__ __forceinline__ float lane_sum(float x)
+{
+    x = with_lane<0xb1>(x);    // the neighbour
+    x = with_lane<0x4e>(x);    // the other pair of four
+    x = with_lane<0x141>(x);   // the other four of eight
+    if (T >= 16) x = with_lane<0x140>(x);   // the other eight of sixteen
+    return across_rows<T>(x);
 }
 
 // Which of the workgroup's rows a thread works on, where T threads share one.

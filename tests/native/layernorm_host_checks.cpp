@@ -77,6 +77,11 @@ hipError_t launch_layernorm_wide(const LayerArgs &, const LayerBackward &b, hipS
     g_back = b;
     return note("wide ");
 }
+hipError_t launch_layernorm_small(const LayerArgs &, const LayerBackward &b, hipStream_t)
+{
+    g_back = b;
+    return note("small ");
+}
 hipError_t launch_layernorm_join(const LayerArgs &, const LayerBackward &b, hipStream_t)
 {
     g_back = b;
@@ -129,7 +134,7 @@ void overlaps()
 void gradients()
 {
     std::mt19937 rng(5);
-    int wide = 0, held = 0;
+    int wide = 0, held = 0, small = 0;
     for (int round = 0; round < 3000; ++round) {
         static const int64_t widths[] = {1, 3, 8, 512, 513, 1024, 1025, 2048, 8192, 8193, 16384, 16385, 100000, 1 << 20};
         ddp_layernorm_desc d = desc_of(widths[rng() % 14]);
@@ -150,8 +155,15 @@ void gradients()
         const bool sums = dw || db;
         std::string want;
         const bool reads_again = d.width > 2048 * ddp::layer_vector(d.x_dtype, d.y_dtype);
-        if (n > 0 && (dx || sums)) want += reads_again ? "wide " : "rows ";
-        if (sums && (n > 0 || !acc)) want += "join ";
+        const int64_t each = (d.x_dtype ? 2 : 4) + (d.y_dtype ? 2 : 4);
+        const int64_t data = n * d.width * each;
+        if (sums && n > 0 && n <= 2048 && !reads_again && data <= 8 << 20 && n * data <= int64_t(1) << 33) {
+            want = "small ";
+            ++small;
+        } else {
+            if (n > 0 && (dx || sums)) want += reads_again ? "wide " : "rows ";
+            if (sums && (n > 0 || !acc)) want += "join ";
+        }
         expect(g_made == want, name + ": launches " + g_made);
         if (!want.empty()) {
             expect((g_back.parts != nullptr) == sums, name + ": parts");
@@ -161,9 +173,13 @@ void gradients()
             (reads_again ? wide : held)++;
         }
     }
-    expect(wide > 100 && held > 100, "gradients: one path hardly taken");
+    expect(wide > 100 && held > 100 && small > 100, "gradients: one path hardly taken");
     ddp_layernorm_desc d = desc_of(16);
     const uintptr_t far = uintptr_t(1) << 40;
+    g_made.clear();   // one launch would read dy while it writes dx there
+    expect(ddp_layernorm_grad(&d, 2, address(far), address(2 * far), nullptr, nullptr, address<float>(3 * far),
+                              address<float>(4 * far), address(far), address(5 * far), nullptr, 0, address(6 * far), 4096,
+                              nullptr) == DDP_OK && g_made == "rows join ", "gradient in dy's place: " + g_made);
     g_stream_device = 1;
     hipStream_t s = static_cast<hipStream_t>(address(0x1000));
     const int before = g_launches;

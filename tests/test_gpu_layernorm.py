@@ -366,6 +366,19 @@ def test_backward_rows(rows, width):
         b.check()
 
 
+@pytest.mark.parametrize("sums", [1, 2, 3])
+@pytest.mark.parametrize("dx", [False, True])
+def test_backward_on_both_sides_of_the_one_launch_path(sums, dx):
+    for rows, width, x, y in ((1, 33, 1, 1), (127, 64, 0, 0), (128, 65, 0, 1), (129, 2000, 2, 2), (513, 300, 1, 1),
+                              (1024, 1024, 0, 0), (1025, 1024, 0, 0), (1024, 2047, 1, 1), (2048, 512, 1, 1),
+                              (2048, 513, 1, 1), (2049, 40, 0, 2), (300, 5000, 1, 1), (60, 16384, 2, 2), (2048, 1, 1, 1)):
+        for acc in (False, True):
+            b = Backward(rows, width, sums % 2, x, y, 0, x if acc else 0, dz=dx, dx=dx, sums=sums, accumulate=acc,
+                         strides=(1, 4, 2), seed=rows)
+            b.run()
+            b.check()
+
+
 def test_backward_of_wide_rows_and_many():
     for rows, width in ((300, 40001), (2000, 16400)):
         b = Backward(rows, width, 0, 0, 0, seed=rows)
