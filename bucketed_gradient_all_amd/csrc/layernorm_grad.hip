@@ -8,7 +8,7 @@
 // it: a row stays in registers between its two sums and dx, and each thread
 // keeps the sums of its columns over all rows that its workgroup takes. Every
 // workgroup leaves one row of such sums (a part), which a second launch adds
-// up: no atomics, and an order that the sizes alone decide. 32768 rows of 2048
+// up: no atomics, and an order that the sizes and types decide. 32768 rows of 2048
 // bf16 values take 87 us and the join 4 (5.8 TB/s together), 2048 rows of 1024 fp32
 // values 6 to 9 and 2 to 3.5.
 #include "layernorm_kernels.h"

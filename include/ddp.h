@@ -789,8 +789,9 @@ size_t ddp_layernorm_grad_workspace_bytes(const ddp_layernorm_desc *desc, int64_
  * dx is the gradient of x, and of add. A NULL dx, dweight or dbias is not
  * computed. With accumulate != 0 dweight and dbias are added to what they
  * hold; otherwise their old contents are not read. Everything is fp32, rounded
- * once; the order of the additions depends on the sizes alone: the same call
- * gives the same bits every time (no floating-point atomics).
+ * once; the order of the additions depends on the sizes, the types and whether
+ * dx takes dy's place: the same call gives the same bits every time (no
+ * floating-point atomics).
  * Pointers as for ddp_layernorm (workspace: 256 bytes; it may be NULL without
  * dweight and dbias). Outputs and workspace must overlap no argument, except
  * that dx may lie exactly where dy or dz does. A workspace serves one call at
