@@ -36,9 +36,12 @@ constexpr RowPlan row_plan(int64_t vectors, bool stream)
 {
     if (vectors > 512) return {512, 1};
     if (vectors > 256) return {512, 2};
+    const int threads = stream ? 256 : 512;
+    // three vectors a thread
+    if (vectors > 64 && vectors <= 96 && stream) return {threads, threads / 32};
+    if (vectors > 128 && vectors <= 192) return {threads, threads / 64};
     int shared = 8;   // threads of a row
     while (shared < vectors) shared *= 2;
-    const int threads = stream ? 256 : 512;
     return {threads, threads / shared * 2};
 }
 

@@ -214,6 +214,12 @@ hipError_t run_rows(const LayerArgs &a, const LayerForward &f, hipStream_t s)
 // one; 8192 109 by four with four, 101 by eight with two, 110 by sixteen with one.
 // Up to 32768 columns in registers: 16384 fp32 ones 215 us, 252 read again; 32768
 // 16-bit ones 118 and 139, but 20000 149 and 141.
+// Where those counts leave a fifth of the threads idle or more, a count nearer to the
+// row: 768 16-bit columns 95 us by half a wave with three vectors (where they come
+// from memory; 5.7 us against 5.3 for 2^21 elements) and 100 by a wave with two, 1536
+// 101 by three waves and 106 by four, 2560 109 by five and 126 by eight; 1280 fp32
+// columns 181 and 198; 5120 16-bit ones 105 and 119, 10240 116 and 122, 12288 108 and
+// 113. Twelve waves for 6144 gained nothing.
 // Narrow rows share a wave: 256 16-bit columns 91 us, 145 with a wave each.
 hipError_t launch_layernorm(const LayerArgs &a, const LayerForward &f, hipStream_t s)
 {
@@ -225,10 +231,16 @@ hipError_t launch_layernorm(const LayerArgs &a, const LayerForward &f, hipStream
         if (vectors <= 16) return run_rows<X, Y, 16, 1, VEC>(a, f, s);
         if (vectors <= 32) return run_rows<X, Y, 32, 1, VEC>(a, f, s);
         if (vectors <= 64) return run_rows<X, Y, 64, 1, VEC>(a, f, s);
+        if (VEC == 8 && a.stream && vectors <= 96) return run_rows<X, Y, VEC == 8 ? 32 : 128, VEC == 8 ? 3 : 1, VEC>(a, f, s);
         if (vectors <= 128) return run_rows<X, Y, VEC == 4 ? 128 : 64, VEC == 4 ? 1 : 2, VEC>(a, f, s);
+        if (vectors <= 192) return run_rows<X, Y, 192, 1, VEC>(a, f, s);
         if (vectors <= 256) return run_rows<X, Y, 256, 1, VEC>(a, f, s);
+        if (vectors <= 320) return run_rows<X, Y, 320, 1, VEC>(a, f, s);
         if (vectors <= 512) return run_rows<X, Y, 512, 1, VEC>(a, f, s);
+        if (vectors <= 640) return run_rows<X, Y, 320, 2, VEC>(a, f, s);
         if (vectors <= 1024) return run_rows<X, Y, 512, 2, VEC>(a, f, s);
+        if (vectors <= 1280) return run_rows<X, Y, 640, 2, VEC>(a, f, s);
+        if (vectors <= 1536) return run_rows<X, Y, 768, 2, VEC>(a, f, s);
         if (vectors <= 2048) return run_rows<X, Y, 1024, 2, VEC>(a, f, s);
         if (vectors <= 4096) return run_rows<X, Y, 1024, 4, VEC>(a, f, s);
         if (VEC == 4 && vectors <= 8192) return run_rows<X, Y, 1024, VEC == 4 ? 8 : 4, VEC>(a, f, s);

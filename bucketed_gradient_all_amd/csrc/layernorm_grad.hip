@@ -474,13 +474,24 @@ hipError_t launch_layernorm_rows(const LayerArgs &a, const LayerBackward &b, hip
         if (vectors <= 16) return run_narrow<X, Y, 16, VEC>(a, b, s);
         if (vectors <= 32) return run_narrow<X, Y, 32, VEC>(a, b, s);
         if (vectors <= 64) return run_narrow<X, Y, 64, VEC>(a, b, s);
+        // three vectors a thread where one would leave threads idle, and then no
+        // barrier: 2^26 bf16 values in rows of 768 95 us against 105, of 1536 98
+        // against 106; 2^21 in rows of 1536 11.5 against 11.9. One vector a thread by
+        // three waves 107 and 14.8; fp32 rows of 384 and 768 183 to 186 us either way
+        if (vectors <= 96 && a.stream) return run_grad<X, Y, 256, 32, 3, 1, true, VEC>(a, b, s);
         if (vectors <= 128) return run_narrow<X, Y, 128, VEC>(a, b, s);
+        if (vectors <= 192)
+            return a.stream ? run_grad<X, Y, 256, 64, 3, 1, true, VEC>(a, b, s)
+                            : run_grad<X, Y, 512, 64, 3, 1, true, VEC>(a, b, s);
         if (vectors <= 256) return run_narrow<X, Y, 256, VEC>(a, b, s);
         // two vectors a thread of 256 against one of 512: 8191 rows of 2047 fp32
         // values 37 us against 47, 2^26 bf16 values in rows of 4096 95 against 102,
         // 2^21 13.7 against 11.3
         if (vectors <= 512) return run_grad<X, Y, 512, 256, 2, 1, true, VEC>(a, b, s);
         if (vectors <= 1024) return run_grad<X, Y, 512, 512, 2, 1, true, VEC>(a, b, s);
+        // 2^26 bf16 values in rows of 12288 105 us, with four vectors a thread 138 and
+        // without the next row ahead 114; fp32 rows of 5120 178, 205 and 198
+        if (vectors <= 1536) return run_grad<X, Y, 512, 512, 3, 1, true, VEC>(a, b, s);
         // 2^26 bf16 values in rows of 16384 131 us; by 1024 threads with two
         // vectors each, which leaves them half the registers, 165
         return run_grad<X, Y, 512, 512, 4, 1, false, VEC>(a, b, s);

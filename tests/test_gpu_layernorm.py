@@ -35,8 +35,10 @@ P = 100
 D = P / 2 + 6
 HALF_SUBNORMAL = {0: 2.0 ** -150, 1: 2.0 ** -134, 2: 2.0 ** -25}
 PAIRS = [(0, 0), (0, 1), (0, 2), (1, 1), (2, 2)]   # x, y
-WIDTHS = [1, 2, 3, 4, 5, 7, 8, 9, 15, 16, 17, 63, 64, 65, 100, 127, 128, 255, 256, 257, 500, 511, 512, 513, 1000, 1023,
-          1024, 1025, 2047, 2048, 2049, 4095, 4096, 4097, 5000, 8191, 8192, 8193, 16383, 16384, 16385, 32767, 32768, 32769, 40001]
+WIDTHS = [1, 2, 3, 4, 5, 7, 8, 9, 15, 16, 17, 63, 64, 65, 100, 127, 128, 255, 256, 257, 380, 500, 511, 512, 513, 640,
+          768, 769, 1000, 1023, 1024, 1025, 1281, 1530, 1537, 2047, 2048, 2049, 2559, 2561, 4095, 4096, 4097, 5000,
+          5119, 5121, 6143, 6145, 8191, 8192, 8193, 10239, 10241, 12287, 12289, 16383, 16384, 16385, 32767, 32768,
+          32769, 40001]
 
 
 def _torch():
@@ -398,7 +400,7 @@ def test_backward_outputs_that_are_not_wanted(sums, dx, accumulate):
             b.check()
 
 
-@pytest.mark.parametrize("width", [5, 100, 2047, 4100, 16391, 33001])
+@pytest.mark.parametrize("width", [5, 100, 751, 1500, 2047, 4100, 10003, 16391, 33001])
 @pytest.mark.parametrize("where", ["dy", "dz"])
 def test_backward_in_place(width, where):
     for kind in (0, 1):
@@ -546,7 +548,8 @@ def test_special_streams():
 
 
 @pytest.mark.parametrize("rows,width,x,y", [(600001, 60, 1, 1), (140001, 250, 0, 0), (70001, 500, 1, 1), (33001, 1001, 0, 2),
-                                            (17001, 2047, 0, 1), (4201, 8100, 2, 2)])
+                                            (17001, 2047, 0, 1), (4201, 8100, 2, 2), (70001, 765, 1, 1), (50001, 380, 0, 2),
+                                            (25001, 1501, 2, 2), (30001, 750, 0, 0), (4001, 10003, 1, 1)])
 def test_large_inputs(rows, width, x, y):
     """Rows that are read past the caches."""
     for kind in (0, 1):
