@@ -197,7 +197,8 @@ struct Plan {
     size_t bytes;      // of the workspace
 };
 
-// Parts at most: eight waves a CU.
+// Parts at most: eight waves on each of 256 CUs, or nine where they are three a
+// workgroup, so that every CU has as many.
 constexpr int64_t kMostThreads = int64_t(512) * 256;
 
 Plan plan_of(const ddp_layernorm_desc &d, int64_t n_rows)
@@ -206,8 +207,8 @@ Plan plan_of(const ddp_layernorm_desc &d, int64_t n_rows)
     const int64_t vec = ddp::layer_vector(d.x_dtype, d.y_dtype);
     const int64_t vectors = std::max<int64_t>(1, ceil_div(d.width, vec));
     p.wide = vectors > ddp::kRowVectors;
-    const ddp::RowPlan r = ddp::row_plan(vectors, streams(d, n_rows));
-    int64_t most = kMostThreads / r.threads, rows = r.rows;
+    const ddp::RowPlan r = ddp::row_plan(vectors, vec, streams(d, n_rows));
+    int64_t most = ceil_div(kMostThreads / r.threads, 256) * 256, rows = r.rows;
     if (p.wide) most = std::max<int64_t>(1, 1024 / ceil_div(vectors, 64)), rows = 4;
     p.n_parts = int32_t(std::min(most, ceil_div(n_rows, rows)));
     p.bytes = (size_t(p.n_parts) * 2 * size_t(d.width) * sizeof(float) + kAlign - 1) / kAlign * kAlign + kAlign;

@@ -27,14 +27,15 @@ constexpr int layer_vector(int x_dtype, int y_dtype)
 // are read again for each pass over them.
 constexpr int kRowVectors = 2048;
 
-// The backward pass's workgroups, by the vectors of a row and whether rows are
-// read past the caches: threads, and rows taken at once.
+// The backward pass's workgroups, by the vectors of a row, their columns and
+// whether rows are read past the caches: threads, and rows taken at once.
 struct RowPlan {
     int threads, rows;
 };
-constexpr RowPlan row_plan(int64_t vectors, bool stream)
+constexpr RowPlan row_plan(int64_t vectors, int64_t vec, bool stream)
 {
     if (vectors > 512) return {512, 1};
+    if (stream && vectors > 256 && vectors <= (vec == 4 ? 320 : 384)) return {192, 1};
     if (vectors > 256) return {512, 2};
     const int threads = stream ? 256 : 512;
     // three vectors a thread

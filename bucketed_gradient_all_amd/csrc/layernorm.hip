@@ -231,7 +231,9 @@ hipError_t launch_layernorm(const LayerArgs &a, const LayerForward &f, hipStream
         if (vectors <= 16) return run_rows<X, Y, 16, 1, VEC>(a, f, s);
         if (vectors <= 32) return run_rows<X, Y, 32, 1, VEC>(a, f, s);
         if (vectors <= 64) return run_rows<X, Y, 64, 1, VEC>(a, f, s);
-        if (VEC == 8 && a.stream && vectors <= 96) return run_rows<X, Y, VEC == 8 ? 32 : 128, VEC == 8 ? 3 : 1, VEC>(a, f, s);
+        if constexpr (VEC == 8) {
+            if (vectors <= 96 && a.stream) return run_rows<X, Y, 32, 3, VEC>(a, f, s);
+        }
         if (vectors <= 128) return run_rows<X, Y, VEC == 4 ? 128 : 64, VEC == 4 ? 1 : 2, VEC>(a, f, s);
         if (vectors <= 192) return run_rows<X, Y, 192, 1, VEC>(a, f, s);
         if (vectors <= 256) return run_rows<X, Y, 256, 1, VEC>(a, f, s);

@@ -444,7 +444,9 @@ hipError_t run_small(const LayerArgs &a, const LayerBackward &b, hipStream_t s)
 template <int X, int Y, int THREADS, int T, int U, int R, bool AHEAD, int VEC>
 hipError_t run_grad(const LayerArgs &a, const LayerBackward &b, hipStream_t s)
 {
-    static_assert(row_plan(T * U, THREADS == 256).threads == THREADS && row_plan(T * U, THREADS == 256).rows == THREADS / T * R,
+    constexpr int vectors = U == 1 ? T : T * U - T / 2 + 1;   // of a row that it is for
+    constexpr RowPlan plan = row_plan(vectors, VEC, THREADS < 512);
+    static_assert(plan.threads == THREADS && plan.rows == THREADS / T * R,
                   "the parts are planned for it");
     hipLaunchKernelGGL((layernorm_grad_rows<X, Y, THREADS, T, U, R, AHEAD, VEC>), dim3(b.n_parts), dim3(THREADS), 0, s,
                        a, b);
@@ -484,6 +486,10 @@ hipError_t launch_layernorm_rows(const LayerArgs &a, const LayerBackward &b, hip
             return a.stream ? run_grad<X, Y, 256, 64, 3, 1, true, VEC>(a, b, s)
                             : run_grad<X, Y, 512, 64, 3, 1, true, VEC>(a, b, s);
         if (vectors <= 256) return run_narrow<X, Y, 256, VEC>(a, b, s);
+        // rows read past the caches by workgroups of three waves: 2^26 bf16 values in
+        // rows of 2560 102 us against 122, of 2880 101 against 115; fp32 rows of 1280
+        // 179 to 185 against 190, but of 1440 199 against 181
+        if (vectors <= (VEC == 4 ? 320 : 384) && a.stream) return run_grad<X, Y, 192, 192, 2, 1, true, VEC>(a, b, s);
         // two vectors a thread of 256 against one of 512: 8191 rows of 2047 fp32
         // values 37 us against 47, 2^26 bf16 values in rows of 4096 95 against 102,
         // 2^21 13.7 against 11.3

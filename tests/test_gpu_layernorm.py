@@ -549,7 +549,7 @@ def test_special_streams():
 
 @pytest.mark.parametrize("rows,width,x,y", [(600001, 60, 1, 1), (140001, 250, 0, 0), (70001, 500, 1, 1), (33001, 1001, 0, 2),
                                             (17001, 2047, 0, 1), (4201, 8100, 2, 2), (70001, 765, 1, 1), (50001, 380, 0, 2),
-                                            (25001, 1501, 2, 2), (30001, 750, 0, 0), (4001, 10003, 1, 1)])
+                                            (25001, 1501, 2, 2), (30001, 750, 0, 0), (4001, 10003, 1, 1), (18001, 2501, 1, 1), (16001, 1150, 0, 0)])
 def test_large_inputs(rows, width, x, y):
     """Rows that are read past the caches."""
     for kind in (0, 1):
