@@ -11,8 +11,7 @@
 // 4.4 ms (6.1 TB/s), with 8-bit states 2.49 ms (6.2 TB/s). Everything is fp32 and
 // every operation is rounded by itself (no product is fused with a sum). With
 // 8-bit states an element takes nearly sixty instructions, two thirds of what the
-// memory's time leaves; the short quotient and root below are for them (with the
-// compiler's 2.58 ms).
+// memory's time leaves; the short quotient below is for them.
 //
 // 8-bit states: the m and r = sqrt(v) of a block of 128 elements are held as
 // e4m3 codes of m * (1 / max|m| * 448), with max|m| * (1 / 448) as the block's scale.
@@ -138,25 +137,13 @@ __device__ __forceinline__ float quotient(float a, float b)
     return __builtin_amdgcn_div_fixupf(q, b, a);   // zeros, infinities and NaN
 }
 
-// sqrt(v) to nearest, for v >= 2^-96; below, off by a unit in the last place or
-// two, but positive for a positive v. The unit's root is off by one unit at
-// most: its neighbours' residuals say whether one of them is nearer.
-__device__ __forceinline__ float root(float v)
-{
-    const float s = __builtin_amdgcn_sqrtf(v);
-    const float lower = __uint_as_float(__float_as_uint(s) - 1), upper = __uint_as_float(__float_as_uint(s) + 1);
-    const float from_lower = __fmaf_rn(-lower, s, v), from_upper = __fmaf_rn(-upper, s, v);
-    const float t = from_lower <= 0.0f ? lower : s;
-    return from_upper > 0.0f ? upper : t;
-}
-
 // One element's step; returns sqrt(v).
 __device__ __forceinline__ float update(const Scalars &c, float g, float &m, float &v, float &p)
 {
     g = __fmul_rn(g, c.f);
     m = __fadd_rn(__fmul_rn(m, c.b1), __fmul_rn(g, c.a1));
     v = __fadd_rn(__fmul_rn(v, c.b2), __fmul_rn(__fmul_rn(g, g), c.a2));
-    const float r = root(v);
+    const float r = sqrtf(v);   // to nearest, for a subnormal v too
     const float d = quotient(m, __fadd_rn(__fmul_rn(r, c.root), c.eps));
     p = __fsub_rn(__fmul_rn(p, c.keep), __fmul_rn(d, c.size));
     return r;

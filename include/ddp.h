@@ -622,8 +622,9 @@ int ddp_adamw_destroy(ddp_adamw *o);
 typedef struct {
     double lr;                /* finite, >= 0                                                       */
     double beta1, beta2;      /* in [0, 1)                                                          */
-    double eps;               /* 0 or a normal, positive fp32 number. With 0 an element without any
-                                 gradient so far is 0 / 0                                            */
+    double eps;               /* 0 or a normal, positive fp32 number. With 0 an element whose second
+                                 moment is 0 is divided by 0: one without any gradient so far, or with
+                                 gradients below about 1e-21, whose squares fp32 does not hold       */
     int64_t step;             /* t, the number of this step, from 1 on                              */
     const float *lr_ptr;      /* device, one float that the step reads instead of lr; or NULL. With it
                                  and step_ptr the replays of a recorded step go on with the schedule */

@@ -1,0 +1,106 @@
+"""GPU: the AdamW step over the whole range of fp32, in both kinds of states, bit
+for bit against the definition's operations in fp32, each rounded by itself:
+gradients whose squares are subnormal. The definition is computed with numpy,
+whose elementwise sums, products, quotients and roots are IEEE operations,
+subnormals included.
+"""
+import math
+
+import numpy as np
+import pytest
+
+from test_gpu_adamw import Case, dequantise, quantise
+
+pytestmark = pytest.mark.gpu
+
+B1, B2, LR = 0.9, 0.999, 1e-3
+SIZES = [5000, 1023, 1024, 1025, 129]
+f32 = np.float32
+
+
+def _torch():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch
+
+
+def definition(g, p, m, v, decay, step, eps, b1=B1, b2=B2, lr=LR):
+    """p, m, v and the root of v after a step."""
+    with np.errstate(all="ignore"):
+        m = m * f32(b1) + g * f32(1.0 - b1)
+        v = v * f32(b2) + (g * g) * f32(1.0 - b2)
+        r = np.sqrt(v)
+        d = m / (r * f32(1.0 / math.sqrt(1.0 - b2 ** step)) + f32(eps))
+        p = p * f32(1.0 - lr * decay) - d * f32(lr / (1.0 - b1 ** step))
+    assert all(x.dtype == f32 for x in (p, m, v, r))
+    return p, m, v, r
+
+
+def same(got, want, what):
+    got, want = got.cpu().numpy(), np.asarray(want)
+    bad = ~((got == want) | (np.isnan(got) & np.isnan(want))) if got.dtype == f32 else got != want
+    assert not bad.any(), (what, int(bad.sum()), [(got[i], want[i]) for i in np.flatnonzero(bad)[:3]])
+
+
+def step_and_compare(c, step, eps, **kw):
+    """One step of the case, and everything it leaves against the definition."""
+    torch = _torch()
+    c.remember()
+    c.step(LR, step, eps=eps, **{"beta1": kw.get("b1", B1), "beta2": kw.get("b2", B2)})
+    torch.cuda.synchronize()
+    for i in range(len(c.sizes)):
+        g, p, m, v, ms, vs = (None if t[i] is None else t[i].cpu() for t in c.old)
+        if c.bits == 8:
+            r = dequantise(v, vs).numpy()
+            m = dequantise(m, ms)
+            with np.errstate(under="ignore"):
+                v = torch.from_numpy(r * r)
+        p, m, v, r = definition(g.numpy(), p.numpy(), m.numpy(), v.numpy(), c.decay[i], step, eps, **kw)
+        same(c.p[i], p, (i, "p"))
+        if c.bits == 32:
+            same(c.m[i], m, (i, "m"))
+            same(c.v[i], v, (i, "v"))
+        else:
+            for x, positive, code, scale, what in ((m, False, c.m[i], c.ms[i], "m"), (r, True, c.v[i], c.vs[i], "v")):
+                codes, scales = quantise(torch.from_numpy(x), positive)
+                same(scale, scales.numpy(), (i, what, "scale"))
+                same(code, codes.numpy(), (i, what, "codes"))
+
+
+def powers(n, lo, hi, gen):
+    """Random values of both signs, their logarithms spread over [lo, hi)."""
+    torch = _torch()
+    x = torch.exp2(torch.rand(n, generator=gen, dtype=torch.float64) * (hi - lo) + lo)
+    return torch.where(torch.rand(n, generator=gen) < 0.5, -x, x).float()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [0.0, 1e-20, 1e-8])
+def test_gradients_whose_squares_are_subnormal(bits, eps):
+    """|g| from 1e-22 to 1e-13: (1 - beta2) g^2 from 0 over the subnormal
+    numbers to 2^-96 and above. From the first step's states on."""
+    torch = _torch()
+    c = Case(SIZES, bits=bits, first=True)
+    gen = torch.Generator().manual_seed(4)
+    for step in (1, 2, 3):
+        for i, n in enumerate(SIZES):
+            c.g[i].copy_(powers(n, math.log2(1e-22), math.log2(1e-13), gen))
+        step_and_compare(c, step, eps)
+
+
+@pytest.mark.parametrize("size", [1e-19, 1e-18, 1e-17, 1e-15])
+def test_the_first_step_is_the_rate_however_small_the_gradient(size):
+    """With eps = 0 the first step is lr, up to the roundings: v = (1 - beta2) g^2
+    is at least 2^-137 here, so a subnormal number's half step, 2^-150, is 2^-13 of
+    it at most and half of that in its root; a dozen others are 2^-24 each."""
+    torch = _torch()
+    for bits in (32, 8):
+        c = Case([1000], bits=bits, first=True, decay=0.0)
+        c.g[0].fill_(size)
+        c.p[0].zero_()
+        c.step(LR, 1, eps=0.0)
+        torch.cuda.synchronize()
+        assert ((c.p[0].double() / -LR - 1.0).abs() <= 2.0 ** -14 + 12 * 2.0 ** -24).all()
+        if bits == 8:   # no root is held as zero beside a first moment that is not
+            assert (c.vs[0] > 0).all() and (c.v[0] > 0).all() and (c.ms[0] > 0).all()
