@@ -9,9 +9,13 @@
 // One pass over memory and no operand used twice, so it is bound by memory: 335M
 // fp32 parameters 1.55 ms (6.1 TB/s), 953M with bf16 gradients and a bf16 copy
 // 4.4 ms (6.1 TB/s), with 8-bit states 2.49 ms (6.2 TB/s). Everything is fp32 and
-// every operation is rounded by itself (no product is fused with a sum). With
-// 8-bit states an element takes nearly sixty instructions, two thirds of what the
-// memory's time leaves; the short quotient below is for them.
+// every operation is rounded by itself (no product is fused with a sum). The
+// root and the quotient are IEEE's over fp32's whole range, overflow and subnormal
+// values included. Shorter ones of 16 instructions instead of 27 (a root without
+// scaling, one correction of the first quotient) are wrong at its ends; an element
+// with 8-bit states takes nearly eighty in all, close to what the memory's time
+// leaves, so they gained 4 us of 91 for 42M elements, and nothing for 953M or with
+// fp32 states.
 //
 // 8-bit states: the m and r = sqrt(v) of a block of 128 elements are held as
 // e4m3 codes of m * (1 / max|m| * 448), with max|m| * (1 / 448) as the block's scale.
@@ -124,19 +128,6 @@ __device__ __forceinline__ bool scalars_of(const AdamArgs &a, double decay, Scal
     return true;
 }
 
-// a / b, to nearest but for the rarest of ties: the remainder of a first quotient
-// corrects it once. Two refinements behind a scaling of both, which make it exact
-// for quotients and divisors near the ends of the range too, are half as many
-// instructions again.
-__device__ __forceinline__ float quotient(float a, float b)
-{
-    float r = __builtin_amdgcn_rcpf(b);
-    r = __fmaf_rn(__fmaf_rn(-b, r, 1.0f), r, r);
-    float q = a * r;
-    q = __fmaf_rn(__fmaf_rn(-b, q, a), r, q);
-    return __builtin_amdgcn_div_fixupf(q, b, a);   // zeros, infinities and NaN
-}
-
 // One element's step; returns sqrt(v).
 __device__ __forceinline__ float update(const Scalars &c, float g, float &m, float &v, float &p)
 {
@@ -144,7 +135,7 @@ __device__ __forceinline__ float update(const Scalars &c, float g, float &m, flo
     m = __fadd_rn(__fmul_rn(m, c.b1), __fmul_rn(g, c.a1));
     v = __fadd_rn(__fmul_rn(v, c.b2), __fmul_rn(__fmul_rn(g, g), c.a2));
     const float r = sqrtf(v);   // to nearest, for a subnormal v too
-    const float d = quotient(m, __fadd_rn(__fmul_rn(r, c.root), c.eps));
+    const float d = __fdiv_rn(m, __fadd_rn(__fmul_rn(r, c.root), c.eps));
     p = __fsub_rn(__fmul_rn(p, c.keep), __fmul_rn(d, c.size));
     return r;
 }
@@ -255,7 +246,7 @@ struct BlockScale {
     {
         const float top = __uint_as_float(top_bits);
         const bool none = top < 0x1p-100f;
-        up = none ? 0.0f : __fmul_rn(quotient(1.0f, top), 448.0f);
+        up = none ? 0.0f : __fmul_rn(__fdiv_rn(1.0f, top), 448.0f);
         down = none ? 0.0f : __fmul_rn(top, 1.0f / 448.0f);
     }
 };

@@ -1,8 +1,8 @@
 """GPU: the AdamW step over the whole range of fp32, in both kinds of states, bit
 for bit against the definition's operations in fp32, each rounded by itself:
-gradients whose squares are subnormal. The definition is computed with numpy,
-whose elementwise sums, products, quotients and roots are IEEE operations,
-subnormals included.
+gradients whose squares are subnormal, quotients that overflow, divisors near the
+ends of the range. The definition is computed with numpy, whose elementwise sums,
+products, quotients and roots are IEEE operations, subnormals included.
 """
 import math
 
@@ -104,3 +104,46 @@ def test_the_first_step_is_the_rate_however_small_the_gradient(size):
         assert ((c.p[0].double() / -LR - 1.0).abs() <= 2.0 ** -14 + 12 * 2.0 ** -24).all()
         if bits == 8:   # no root is held as zero beside a first moment that is not
             assert (c.vs[0] > 0).all() and (c.v[0] > 0).all() and (c.ms[0] > 0).all()
+
+
+@pytest.mark.parametrize("eps", [0.0, 2e-38, 1e-8, 1.0, 3e38])
+@pytest.mark.parametrize("b2", [0.0, B2])
+def test_every_magnitude_of_32_bit_states(eps, b2):
+    torch = _torch()
+    c = Case([200003], bits=32)
+    gen = torch.Generator().manual_seed(5)
+    n = 200003
+    c.m[0].copy_(powers(n, -149, 128, gen))
+    v = powers(n, -149, 128, gen).abs()
+    v[::17] = 0.0
+    c.v[0].copy_(v)
+    g = powers(n, -149, 128, gen)
+    g[::3] = 0.0
+    c.g[0].copy_(g)
+    c.p[0][::5] = 0.0
+    step_and_compare(c, 2, eps, b2=b2)
+
+
+@pytest.mark.parametrize("eps", [0.0, 2e-38, 1e-8, 1.0, 3e38])
+@pytest.mark.parametrize("b1,b2", [(B1, B2), (0.0, 0.0)])
+def test_every_magnitude_of_8_bit_states(eps, b1, b2):
+    """Blocks of 128 at magnitudes of their own; squares that stay finite, so
+    that all states do."""
+    torch = _torch()
+    blocks = 1500
+    n = blocks * 128 - 5
+    c = Case([n], bits=8)
+    gen = torch.Generator().manual_seed(6)
+
+    def of(lo, hi):
+        size = powers(blocks, lo, hi - 1, gen).abs().repeat_interleave(128)[:n]
+        return powers(n, -14, 0, gen) * size
+
+    for x, positive, code, scale in ((of(-100, 127), False, c.m[0], c.ms[0]), (of(-74, 62).abs(), True, c.v[0], c.vs[0])):
+        new = quantise(x, positive)
+        code.copy_(new[0])
+        scale.copy_(new[1])
+    g = of(-130, 62)
+    g[::3] = 0.0
+    c.g[0].copy_(g)
+    step_and_compare(c, 2, eps, b1=b1, b2=b2)
