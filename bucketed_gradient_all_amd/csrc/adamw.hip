@@ -1,6 +1,6 @@
 // One AdamW step over a list of tensors.
 //
-//   g = grad * f,  f = min(1, 1 / (norm + 1e-6) * max_norm), or 1 without a norm
+//   g = grad * f,  f = min(1, max_norm / (norm + 1e-6)), or 1 without a norm
 //   m = beta1 * m + (1 - beta1) * g
 //   v = beta2 * v + (1 - beta2) * g^2
 //   p = p * (1 - lr * decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
@@ -103,10 +103,7 @@ __device__ __forceinline__ bool scalars_of(const AdamArgs &a, double decay, Scal
     if (a.norm) {
         const float n = *(const CONSTANT float *)a.norm;
         if (a.skip && !(fabsf(n) < INFINITY)) return false;
-        if (a.max_norm < INFINITY) {
-            const float f = __fmul_rn(__fdiv_rn(1.0f, __fadd_rn(n, 1e-6f)), a.max_norm);
-            c->f = f >= 1.0f ? 1.0f : f;   // a NaN stays one
-        }
+        if (a.max_norm < INFINITY) c->f = clip_factor(a.max_norm, n);
     }
     if (a.lr_ptr || a.step_ptr) {
         // one wave's 64-bit powers for the workgroup: 42M elements with 8-bit

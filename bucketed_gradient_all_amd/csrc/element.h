@@ -61,5 +61,12 @@ __device__ __forceinline__ typename Raw<TYPE, 1>::elem narrow(float v)
     }
 }
 
+// What gradients are scaled by, wherever they are clipped. A NaN stays one.
+__device__ __forceinline__ float clip_factor(float max_norm, float norm)
+{
+    const float f = __fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f));
+    return f >= 1.0f ? 1.0f : f;
+}
+
 }  // namespace
 }  // namespace ddp

@@ -140,12 +140,6 @@ __device__ __forceinline__ double merged_partials(const double *partials, int n)
     return over_workgroup<NORM, THREADS>(v);
 }
 
-__device__ __forceinline__ float clip_factor(float max_norm, float norm)
-{
-    const float f = __fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f));
-    return f >= 1.0f ? 1.0f : f;
-}
-
 // One tile into the running norm. All loads of a thread are issued before the
 // first value is used.
 template <int NORM, int TYPE, int THREADS>

@@ -637,7 +637,7 @@ typedef struct {
 } ddp_adamw_args;
 
 /* One step of every tensor, on `stream`:
- *   g = grad * f,  f = min(1, 1 / (norm + 1e-6) * max_norm), or 1 without a norm
+ *   g = grad * f,  f = min(1, max_norm / (norm + 1e-6)), as ddp_clip_grads scales, or 1 without a norm
  *   m = beta1 * m + (1 - beta1) * g
  *   v = beta2 * v + (1 - beta2) * g^2
  *   p = p * (1 - lr * weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
