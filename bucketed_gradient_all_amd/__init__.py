@@ -11,6 +11,7 @@ no fallback: if libddp.so is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import subprocess
 import threading
@@ -940,10 +941,10 @@ def ddp_adamw_destroy(o: AdamW) -> None:
 
 
 def ddp_adamw_step(o: AdamW, lr: float, step: int, stream: int, beta1: float = 0.9, beta2: float = 0.999,
-                   eps: float = 1e-8, max_norm: float = 0.0, norm: int = 0, skip_nonfinite: bool = False,
+                   eps: float = 1e-8, max_norm: float = math.inf, norm: int = 0, skip_nonfinite: bool = False,
                    lr_ptr: int = 0, step_ptr: int = 0) -> None:
     """norm, lr_ptr and step_ptr: device pointers (float, float, int64); with
-    the last two lr and step are not read."""
+    the last two lr and step are not read. Without max_norm a norm does not clip."""
     a = ddp_adamw_args(lr, beta1, beta2, eps, step, lr_ptr or None, step_ptr or None, norm or None, max_norm,
                        1 if skip_nonfinite else 0)
     o.used_on(stream)

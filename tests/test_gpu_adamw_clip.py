@@ -1,5 +1,8 @@
 """GPU: the AdamW step's clipping is the library's: the factor is the one that
-ddp_clip_grads scales gradients by, bit for bit."""
+ddp_clip_grads scales gradients by, bit for bit, and no bound is applied unless
+one is given."""
+import math
+
 import pytest
 
 from test_gpu_adamw import Case
@@ -51,3 +54,19 @@ def test_a_bound_of_the_norm_itself_leaves_gradients_as_they_are(bits):
         a.step(1e-3, 10, norm=norm.data_ptr(), max_norm=float(norm + 1e-6))
         torch.cuda.synchronize()
         assert torch.equal(a.p[0], b.p[0]) and torch.equal(a.m[0], b.m[0]) and torch.equal(a.v[0], b.v[0]), float(norm)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_norm_without_a_bound_only_decides_whether_to_step(bits):
+    torch = _torch()
+    a, b = (Case([1025], bits=bits, seed=4) for _ in range(2))
+    b.step(1e-3, 10)
+    norm = torch.tensor([1e3], device="cuda")
+    a.step(1e-3, 10, norm=norm.data_ptr(), skip_nonfinite=True)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(a.contents(), b.contents()))
+    a.restore()
+    norm.fill_(math.nan)
+    a.step(1e-3, 10, norm=norm.data_ptr(), skip_nonfinite=True)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(a.before, a.contents()))
