@@ -32,7 +32,7 @@ namespace {
 
 constexpr size_t kAlign = 16;
 
-// Tiles of a list, at most: 2^41 elements.
+// Tiles of a list, at most: 2^40 elements.
 constexpr int64_t kMostTiles = int64_t(1) << 30;
 
 size_t align_up(size_t x)

@@ -11,7 +11,7 @@ namespace ddp {
 // Elements of one tile: four a thread of a workgroup of 256. 953M elements with
 // a copy take 4.66 ms, against 4.87 with tiles of 2048 and 4.60 with tiles of 512
 // (128 threads); with 8-bit states 2.58, 2.70 and 2.60 ms, and 161 odd tensors of
-// 25M elements 83, 87 and 89 us. A list of eight tensors is a launch of 33 tiles
+// 25M elements 83, 87 and 89 us. A list of eight tensors is a launch of 34 tiles
 // (3.2 us in a graph; tiles of 2048 4.3).
 constexpr int kAdamTile = 1024;
 
@@ -25,7 +25,7 @@ enum AdamOut : uint8_t { kParamF32, kParamF32CopyBF16, kParamF32CopyF16, kParamB
 // One tensor. With 32-bit states its tiles are cut at parameter addresses that
 // are multiples of 256 bytes, so that full tiles store whole cache lines: tile
 // k covers elements [k * kAdamTile - shift, (k + 1) * kAdamTile - shift) of it.
-// With 8-bit states shift is 0 and a tile holds sixteen whole blocks.
+// With 8-bit states shift is 0 and a tile holds eight whole blocks.
 struct AdamSeg {
     const void *grad;
     void *param;

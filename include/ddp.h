@@ -599,16 +599,17 @@ typedef struct {
 } ddp_adamw_desc;
 
 /* Device workspace a list needs for its tables (80 bytes a tensor, 4 bytes per
- * 2048 elements). Returns 0 and sets ddp_last_error() if the desc is invalid;
- * pointers are not looked at. */
+ * 1024 elements and 8 for each tensor's ends). Returns 0 and sets
+ * ddp_last_error() if the desc is invalid; pointers are not looked at. */
 size_t ddp_adamw_workspace_bytes(const ddp_adamw_desc *desc);
 
 /* Builds the list's tables and uploads them (synchronously) into the
  * workspace, as ddp_grads_create does (45 us for 8 tensors through the Python
  * binding, 80 to 130 for several hundred or a quarter of a billion elements),
- * under the same rules: workspace and tensors stay valid for as long as the list, or a graph that recorded a step,
- * is used; not while a stream is being recorded; tied to the device that is
- * current here. *out is set only on success.
+ * under the same rules: workspace and tensors stay valid for as long as the
+ * list, or a graph that recorded a step, is used; not while a stream is being
+ * recorded; tied to the device that is current here. *out is set only on
+ * success.
  * Errors: DDP_ERR_INVALID: bad sizes, types, decays or alignment; a copy
  * beside 16-bit parameters; a range that overlaps another of the tensors' or
  * the workspace (gradients may share memory with each other: they are only
