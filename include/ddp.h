@@ -775,7 +775,7 @@ int ddp_layernorm(const ddp_layernorm_desc *desc, int64_t n_rows, const void *x,
                   const void *bias, void *z, void *y, float *mean, float *rstd, void *stream);
 
 /* Device workspace of one ddp_layernorm_grad call of up to n_rows rows: partial
- * sums, at most 512 times dweight and dbias in fp32. Small calls go in one launch
+ * sums, at most 768 times dweight and dbias in fp32. Small calls go in one launch
  * that does not touch it, but it is asked for all the same. Returns 0 and sets
  * ddp_last_error() if the desc is invalid. */
 size_t ddp_layernorm_grad_workspace_bytes(const ddp_layernorm_desc *desc, int64_t n_rows);
