@@ -207,13 +207,33 @@ hipError_t run_rows(const LayerArgs &a, const LayerForward &f, hipStream_t s)
 
 }  // namespace
 
+// Whether rows of 2049 to 8192 vectors are read again for each pass instead of kept
+// in registers, four or eight vectors a thread. Where a row has few more vectors
+// than the next smaller count holds, half of the threads' registers stay empty, and
+// reading x again from L2 costs less; not with 256 rows or fewer, where each CU has
+// one and waits for it three times. Of 2^26 elements without add, kept and read
+// again: 16-bit rows of 16392 columns 112 and 88 us, of 28000 88 and 86, of 30000 83
+// and 86 (320 rows: 13.3 and 10.8, 14.0 and 14.8, 14.4 and 15.4; 256 rows 8.1 and
+// 8.3, 8.3 and 10.6); fp32 rows of 8200 158 and 135, of 11000 135 and 135, of 12000
+// 128 and 134; into 16 bits of 16400 133 and 126, of 20000 124 and 125, but into fp32
+// of 18000 93 and 99 (2560 rows). With add all passes but the first read z: 16-bit
+// rows past the caches of 16392 165 and 148, of 20000 149 and 141, of 22000 141 and
+// 143; from the caches 37 and 38, fp32 ones of 8200 230 and 257.
+bool reads_again(const LayerArgs &a, const LayerForward &f, int64_t vectors, int vec)
+{
+    if (f.add) return vec == 8 && a.stream && f.z && vectors <= 2600;
+    if (a.rows <= 256) return false;
+    if (vec == 8) return vectors <= 3500;
+    return vectors <= 2700 || (a.y_dtype != DDP_F32 && vectors > 4096 && vectors <= 4500);
+}
+
 // A vector a thread, or two where that makes more waves than it saves: of 2^26
 // elements with weight and bias, 1024 16-bit columns take 92 us by one wave with
 // two vectors and 95 by two with one, 512 fp32 columns 186 and 173; 4096 16-bit
 // columns 143 us by one wave with eight, 101 by four with two, 100 by eight with
 // one; 8192 109 by four with four, 101 by eight with two, 110 by sixteen with one.
-// Up to 32768 columns in registers: 16384 fp32 ones 215 us, 252 read again; 32768
-// 16-bit ones 118 and 139, but 20000 149 and 141.
+// Up to 32768 columns in registers: with add 16384 fp32 ones 206 us, 252 read
+// again; 32768 16-bit ones 122 and 141.
 // Where those counts leave a fifth of the threads idle or more, a count nearer to the
 // row: 768 16-bit columns 95 us by half a wave with three vectors (where they come
 // from memory; 5.7 us against 5.3 for 2^21 elements) and 100 by a wave with two, 1536
@@ -244,8 +264,10 @@ hipError_t launch_layernorm(const LayerArgs &a, const LayerForward &f, hipStream
         if (vectors <= 1280) return run_rows<X, Y, 640, 2, VEC>(a, f, s);
         if (vectors <= 1536) return run_rows<X, Y, 768, 2, VEC>(a, f, s);
         if (vectors <= 2048) return run_rows<X, Y, 1024, 2, VEC>(a, f, s);
-        if (vectors <= 4096) return run_rows<X, Y, 1024, 4, VEC>(a, f, s);
-        if (VEC == 4 && vectors <= 8192) return run_rows<X, Y, 1024, VEC == 4 ? 8 : 4, VEC>(a, f, s);
+        if (!reads_again(a, f, vectors, VEC)) {
+            if (vectors <= 4096) return run_rows<X, Y, 1024, 4, VEC>(a, f, s);
+            if (VEC == 4 && vectors <= 8192) return run_rows<X, Y, 1024, VEC == 4 ? 8 : 4, VEC>(a, f, s);
+        }
         return over_rows(a.rows, 1, [&](dim3 g, int64_t first) {
             hipLaunchKernelGGL((layernorm_wide<X, Y, VEC>), g, dim3(1024), 0, s, a, f, first);
         });
