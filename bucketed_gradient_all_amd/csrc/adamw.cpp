@@ -262,6 +262,8 @@ int step(const ddp_adamw *o, const ddp_adamw_args *a, hipStream_t s)
     if (a->eps != 0.0 && !std::isnormal(float(a->eps)))
         return fail(DDP_ERR_INVALID, "eps must be 0 or a normal fp32 number");
     if (a->eps < 0.0) return fail(DDP_ERR_INVALID, "eps must not be negative");
+    // the short quotient takes divisors of up to 2^126; sqrt(v) * root stays below 2^91
+    if (o->tables.bits == 8 && a->eps > 0x1p125) return fail(DDP_ERR_INVALID, "eps with 8-bit states must be at most 2^125");
     if (bad_rate(a->beta1) || bad_rate(a->beta2)) return fail(DDP_ERR_INVALID, "beta1 and beta2 must be in [0, 1)");
     if (!a->step_ptr && a->step < 1) return fail(DDP_ERR_INVALID, "step counts from 1");
     if (a->norm && !(a->max_norm >= 0.0f)) return fail(DDP_ERR_INVALID, "max_norm must not be negative");

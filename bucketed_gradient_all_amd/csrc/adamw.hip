@@ -10,12 +10,9 @@
 // fp32 parameters 1.55 ms (6.1 TB/s), 953M with bf16 gradients and a bf16 copy
 // 4.4 ms (6.1 TB/s), with 8-bit states 2.49 ms (6.2 TB/s). Everything is fp32 and
 // every operation is rounded by itself (no product is fused with a sum). The
-// root and the quotient are IEEE's over fp32's whole range, overflow and subnormal
-// values included. Shorter ones of 16 instructions instead of 27 (a root without
-// scaling, one correction of the first quotient) are wrong at its ends; an element
-// with 8-bit states takes nearly eighty in all, close to what the memory's time
-// leaves, so they gained 4 us of 91 for 42M elements, and nothing for 953M or with
-// fp32 states.
+// root and the quotient are IEEE's over fp32's whole range, but for the quotient of
+// the 8-bit step (below): an element takes some seventy-five instructions there,
+// close to what the memory's time leaves.
 //
 // 8-bit states: the m and r = sqrt(v) of a block of 128 elements are held as
 // e4m3 codes of m * (1 / max|m| * 448), with max|m| * (1 / 448) as the block's scale.
@@ -35,6 +32,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 
 namespace ddp {
 namespace {
@@ -125,14 +123,33 @@ __device__ __forceinline__ bool scalars_of(const AdamArgs &a, double decay, Scal
     return true;
 }
 
+// a / b for b in [0, 2^126]: the remainder of a first quotient corrects it once, to
+// nearest, or beside it where a / b lies all but in the middle of two values (it
+// equals IEEE division for every reciprocal and for 2^31 random quotients). Where the remainder is subnormal (|a| below
+// 2^-100) the quotient is off by two units in its last place at most. A first quotient beyond
+// fp32's range is held at its end, from where the correction leaves it where it
+// belongs. IEEE division, scaled and corrected twice, takes four instructions more:
+// 42M elements with 8-bit states 90 us against 87.5, with the schedule on the
+// device 101 against 98, 953M 2.62 ms against 2.55; with 32-bit states it is free.
+__device__ __forceinline__ float quotient(float a, float b)
+{
+    float r = __builtin_amdgcn_rcpf(b);
+    r = __fmaf_rn(__fmaf_rn(-b, r, 1.0f), r, r);
+    float q = __builtin_amdgcn_fmed3f(a * r, -FLT_MAX, FLT_MAX);
+    q = __fmaf_rn(__fmaf_rn(-b, q, a), r, q);
+    return __builtin_amdgcn_div_fixupf(q, b, a);   // zeros, infinities and NaN
+}
+
 // One element's step; returns sqrt(v).
+template <int BITS>
 __device__ __forceinline__ float update(const Scalars &c, float g, float &m, float &v, float &p)
 {
     g = __fmul_rn(g, c.f);
     m = __fadd_rn(__fmul_rn(m, c.b1), __fmul_rn(g, c.a1));
     v = __fadd_rn(__fmul_rn(v, c.b2), __fmul_rn(__fmul_rn(g, g), c.a2));
     const float r = sqrtf(v);   // to nearest, for a subnormal v too
-    const float d = __fdiv_rn(m, __fadd_rn(__fmul_rn(r, c.root), c.eps));
+    const float b = __fadd_rn(__fmul_rn(r, c.root), c.eps);
+    const float d = BITS == 32 ? __fdiv_rn(m, b) : quotient(m, b);
     p = __fsub_rn(__fmul_rn(p, c.keep), __fmul_rn(d, c.size));
     return r;
 }
@@ -158,7 +175,7 @@ __device__ __forceinline__ void step_32(const CONSTANT AdamSeg &s, int64_t base,
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
         x[j] = widen<T::param>(p[j]), y[j] = m[j], z[j] = v[j];
-        update(c, widen<GRAD>(g[j]), y[j], z[j], x[j]);
+        update<32>(c, widen<GRAD>(g[j]), y[j], z[j], x[j]);
     }
     store<T::param>(s.param, e, n, x);
     if constexpr (T::copy >= 0) store<T::copy>(s.copy, e, n, x);
@@ -237,13 +254,15 @@ __device__ __forceinline__ float of_pair(float x)
 // Of a block's largest magnitude: what its values are multiplied with before
 // they are rounded to codes, and the scale that undoes it. A block whose
 // largest is below 2^-100, where 1 / top * 448 could overflow, is held as zeros.
+// top is divided by 256 before and 448 after, both exactly: the reciprocal is then
+// normal up to fp32's end (beyond 2^126 it is not rounded to a subnormal number).
 struct BlockScale {
     float up, down;
     __device__ __forceinline__ explicit BlockScale(uint32_t top_bits)
     {
         const float top = __uint_as_float(top_bits);
         const bool none = top < 0x1p-100f;
-        up = none ? 0.0f : __fmul_rn(__fdiv_rn(1.0f, top), 448.0f);
+        up = none ? 0.0f : __fmul_rn(quotient(1.0f, top * 0x1p-8f), 448.0f * 0x1p-8f);
         down = none ? 0.0f : __fmul_rn(top, 1.0f / 448.0f);
     }
 };
@@ -278,9 +297,9 @@ __device__ __forceinline__ void step_8(const CONSTANT AdamSeg &s, int64_t base, 
     for (int j = 0; j < kVec; ++j) {
         x[j] = widen<T::param>(p[j]);
         float z = __fmul_rn(r[j], r[j]);
-        r[j] = update(c, widen<GRAD>(g[j]), y[j], z, x[j]);
+        r[j] = update<8>(c, widen<GRAD>(g[j]), y[j], z, x[j]);
         top_m = max(top_m, __float_as_uint(y[j]) & 0x7fffffffu);
-        top_r = max(top_r, __float_as_uint(r[j]) & 0x7fffffffu);
+        top_r = max(top_r, __float_as_uint(r[j]));   // not negative; a NaN of either sign is above all
     }
     store<T::param>(s.param, e, n, x);
     if constexpr (T::copy >= 0) store<T::copy>(s.copy, e, n, x);

@@ -623,7 +623,8 @@ int ddp_adamw_destroy(ddp_adamw *o);
 typedef struct {
     double lr;                /* finite, >= 0                                                       */
     double beta1, beta2;      /* in [0, 1)                                                          */
-    double eps;               /* 0 or a normal, positive fp32 number. With 0 an element whose second
+    double eps;               /* 0 or a normal, positive fp32 number, with 8-bit states at most 2^125.
+                                 With 0 an element whose second
                                  moment is 0 is divided by 0: one without any gradient so far, or with
                                  gradients below about 1e-21, whose squares fp32 does not hold       */
     int64_t step;             /* t, the number of this step, from 1 on                              */
@@ -642,8 +643,10 @@ typedef struct {
  *   m = beta1 * m + (1 - beta1) * g
  *   v = beta2 * v + (1 - beta2) * g^2
  *   p = p * (1 - lr * weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
- * in fp32, each operation rounded by itself; the factors that no element
- * enters (powers, 1 - lr * weight_decay) in 64 bits and rounded once. Without
+ * in fp32, each operation rounded by itself (with 8-bit states the quotient of m
+ * may be off by a unit in its last place, by two for |m| below 2^-100); the
+ * factors that no element enters (powers, 1 - lr * weight_decay) in 64 bits and
+ * rounded once. Without
  * skip_nonfinite a norm that is not finite goes into the gradients as in
  * ddp_clip_grad_norm. Gradients are only read. Steps of one list change its
  * tensors and must not run at once; otherwise a list is only read, from any

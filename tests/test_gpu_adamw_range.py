@@ -3,6 +3,11 @@ for bit against the definition's operations in fp32, each rounded by itself:
 gradients whose squares are subnormal, quotients that overflow, divisors near the
 ends of the range. The definition is computed with numpy, whose elementwise sums,
 products, quotients and roots are IEEE operations, subnormals included.
+
+With 8-bit states the quotient d of a first moment m may be off: by a unit in its
+last place, rarely, and by two where |m| is below 2^-100, at most 2^-22 of it or
+2^-148. The product with the step's size and the difference then round each side
+once: u = 2^-24 of each value for each side.
 """
 import math
 
@@ -26,21 +31,35 @@ def _torch():
 
 
 def definition(g, p, m, v, decay, step, eps, b1=B1, b2=B2, lr=LR):
-    """p, m, v and the root of v after a step."""
+    """p, m, v, the root of v and the quotient of a step."""
     with np.errstate(all="ignore"):
         m = m * f32(b1) + g * f32(1.0 - b1)
         v = v * f32(b2) + (g * g) * f32(1.0 - b2)
         r = np.sqrt(v)
         d = m / (r * f32(1.0 / math.sqrt(1.0 - b2 ** step)) + f32(eps))
         p = p * f32(1.0 - lr * decay) - d * f32(lr / (1.0 - b1 ** step))
-    assert all(x.dtype == f32 for x in (p, m, v, r))
-    return p, m, v, r
+    assert all(x.dtype == f32 for x in (p, m, v, r, d))
+    return p, m, v, r, d
 
 
 def same(got, want, what):
     got, want = got.cpu().numpy(), np.asarray(want)
     bad = ~((got == want) | (np.isnan(got) & np.isnan(want))) if got.dtype == f32 else got != want
     assert not bad.any(), (what, int(bad.sum()), [(got[i], want[i]) for i in np.flatnonzero(bad)[:3]])
+
+
+def near(got, want, d, size, m, what):
+    """A parameter stepped by a quotient of the 8-bit step."""
+    got, want, d, m = (np.asarray(x, np.float64) for x in (got.cpu().numpy(), want, d, m))
+    with np.errstate(all="ignore"):
+        err = size * (2.0 ** -22 * np.abs(d) + 2.0 ** -148) * 1.01
+        err += 2 * 2.0 ** -24 * 1.01 * (size * np.abs(d) + np.abs(want)) + 2.0 ** -148
+        equal = (got == want) | (np.isnan(got) & np.isnan(want))
+        end = np.abs(d) >= float(np.finfo(f32).max) * (1 - 2.0 ** -22)   # one side may be beyond the range
+        ok = equal | (np.abs(got - want) <= err) | (end & (np.isinf(got) | np.isinf(want)))
+    assert ok.all(), (what, int((~ok).sum()), [(got[i], want[i], d[i], m[i]) for i in np.flatnonzero(~ok)[:3]])
+    usual = (m == 0) | (np.abs(m) >= 2.0 ** -100)
+    assert (~equal & usual).sum() <= 1e-3 * got.size, what
 
 
 def step_and_compare(c, step, eps, **kw):
@@ -56,12 +75,13 @@ def step_and_compare(c, step, eps, **kw):
             m = dequantise(m, ms)
             with np.errstate(under="ignore"):
                 v = torch.from_numpy(r * r)
-        p, m, v, r = definition(g.numpy(), p.numpy(), m.numpy(), v.numpy(), c.decay[i], step, eps, **kw)
-        same(c.p[i], p, (i, "p"))
+        p, m, v, r, d = definition(g.numpy(), p.numpy(), m.numpy(), v.numpy(), c.decay[i], step, eps, **kw)
         if c.bits == 32:
+            same(c.p[i], p, (i, "p"))
             same(c.m[i], m, (i, "m"))
             same(c.v[i], v, (i, "v"))
         else:
+            near(c.p[i], p, d, LR / (1.0 - kw.get("b1", B1) ** step), m, (i, "p"))
             for x, positive, code, scale, what in ((m, False, c.m[i], c.ms[i], "m"), (r, True, c.v[i], c.vs[i], "v")):
                 codes, scales = quantise(torch.from_numpy(x), positive)
                 same(scale, scales.numpy(), (i, what, "scale"))
@@ -124,7 +144,7 @@ def test_every_magnitude_of_32_bit_states(eps, b2):
     step_and_compare(c, 2, eps, b2=b2)
 
 
-@pytest.mark.parametrize("eps", [0.0, 2e-38, 1e-8, 1.0, 3e38])
+@pytest.mark.parametrize("eps", [0.0, 2e-38, 1e-8, 1.0, 2.0 ** 125])
 @pytest.mark.parametrize("b1,b2", [(B1, B2), (0.0, 0.0)])
 def test_every_magnitude_of_8_bit_states(eps, b1, b2):
     """Blocks of 128 at magnitudes of their own; squares that stay finite, so
