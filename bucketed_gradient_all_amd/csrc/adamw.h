@@ -8,11 +8,12 @@
 
 namespace ddp {
 
-// Elements of one tile: four a thread of a workgroup of 256. 953M elements with
-// a copy take 4.66 ms, against 4.87 with tiles of 2048 and 4.60 with tiles of 512
-// (128 threads); with 8-bit states 2.58, 2.70 and 2.60 ms, and 161 odd tensors of
-// 25M elements 83, 87 and 89 us. A list of eight tensors is a launch of 34 tiles
-// (3.2 us in a graph; tiles of 2048 4.3).
+// Elements of one tile: four a thread of a workgroup of 256. With eight workgroups
+// a CU, and codes that went past the caches, 953M elements with a copy took 4.66 ms,
+// against 4.87 with tiles of 2048 and 4.60 with tiles of 512 (128 threads); with
+// 8-bit states 2.58, 2.70 and 2.60 ms, and 161 odd tensors of 25M elements 83, 87
+// and 89 us. A list of eight tensors is a launch of 34 tiles (3.3 us in a graph;
+// tiles of 2048 4.3).
 constexpr int kAdamTile = 1024;
 
 // Elements of the 8-bit states that share a scale.

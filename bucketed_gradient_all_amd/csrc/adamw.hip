@@ -105,8 +105,8 @@ __device__ __forceinline__ bool scalars_of(const AdamArgs &a, double decay, Scal
     }
     if (a.lr_ptr || a.step_ptr) {
         // one wave's 64-bit powers for the workgroup: 42M elements with 8-bit
-        // states 113 us, against 143 with all four waves' (and 87 to 100 with
-        // the host's scalars); 953M 2.51 ms against 2.72 and 2.50
+        // states 94 to 98 us at step 2000, 86 with the host's scalars; 953M 2.55
+        // ms and 2.48 (all four waves' powers took a quarter and a tenth more)
         __shared__ float found[2];
         if (a.lr_ptr) lr = double(*(const CONSTANT float *)a.lr_ptr);
         if (threadIdx.x < 64) {
@@ -125,12 +125,13 @@ __device__ __forceinline__ bool scalars_of(const AdamArgs &a, double decay, Scal
 
 // a / b for b in [0, 2^126]: the remainder of a first quotient corrects it once, to
 // nearest, or beside it where a / b lies all but in the middle of two values (it
-// equals IEEE division for every reciprocal and for 2^31 random quotients). Where the remainder is subnormal (|a| below
-// 2^-100) the quotient is off by two units in its last place at most. A first quotient beyond
-// fp32's range is held at its end, from where the correction leaves it where it
-// belongs. IEEE division, scaled and corrected twice, takes four instructions more:
-// 42M elements with 8-bit states 90 us against 87.5, with the schedule on the
-// device 101 against 98, 953M 2.62 ms against 2.55; with 32-bit states it is free.
+// equals IEEE division for every reciprocal and for 2^31 random quotients). Where
+// the remainder is subnormal (|a| below 2^-100) the quotient is off by two units in
+// its last place at most. A first quotient beyond fp32's range is held at its end,
+// from where the correction leaves it where it belongs. IEEE division, scaled and
+// corrected twice, takes four instructions more: 42M elements with 8-bit states 90
+// us against 87.5, with the schedule on the device 101 against 98, 953M 2.62 ms
+// against 2.55; with 32-bit states it is free.
 __device__ __forceinline__ float quotient(float a, float b)
 {
     float r = __builtin_amdgcn_rcpf(b);

@@ -498,8 +498,9 @@ hipError_t launch_layernorm_rows(const LayerArgs &a, const LayerBackward &b, hip
         // 2^26 bf16 values in rows of 12288 105 us, with four vectors a thread 138 and
         // without the next row ahead 114; fp32 rows of 5120 178, 205 and 198
         if (vectors <= 1536) return run_grad<X, Y, 512, 512, 3, 1, true, VEC>(a, b, s);
-        // 2^26 bf16 values in rows of 16384 131 us; by 1024 threads with two
-        // vectors each, which leaves them half the registers, 165
+        // 2^26 bf16 values in rows of 16384 131 us, with all 256 registers taken and
+        // 16 to 19 spilled; by 1024 threads with two vectors each, which leaves them
+        // half the registers, 165
         return run_grad<X, Y, 512, 512, 4, 1, false, VEC>(a, b, s);
     });
 }
