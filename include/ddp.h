@@ -624,9 +624,9 @@ typedef struct {
     double lr;                /* finite, >= 0                                                       */
     double beta1, beta2;      /* in [0, 1)                                                          */
     double eps;               /* 0 or a normal, positive fp32 number, with 8-bit states at most 2^125.
-                                 With 0 an element whose second
-                                 moment is 0 is divided by 0: one without any gradient so far, or with
-                                 gradients below about 1e-21, whose squares fp32 does not hold       */
+                                 With 0 an element whose second moment is 0 is divided by 0: one
+                                 without any gradient so far, or with gradients below about 1e-21,
+                                 whose squares fp32 does not hold                                    */
     int64_t step;             /* t, the number of this step, from 1 on                              */
     const float *lr_ptr;      /* device, one float that the step reads instead of lr; or NULL. With it
                                  and step_ptr the replays of a recorded step go on with the schedule */
@@ -646,11 +646,10 @@ typedef struct {
  * in fp32, each operation rounded by itself (with 8-bit states the quotient of m
  * may be off by a unit in its last place, by two for |m| below 2^-100); the
  * factors that no element enters (powers, 1 - lr * weight_decay) in 64 bits and
- * rounded once. Without
- * skip_nonfinite a norm that is not finite goes into the gradients as in
- * ddp_clip_grad_norm. Gradients are only read. Steps of one list change its
- * tensors and must not run at once; otherwise a list is only read, from any
- * stream and replayed graph. May be recorded into a HIP graph.
+ * rounded once. Without skip_nonfinite a norm that is not finite goes into the
+ * gradients as in ddp_clip_grad_norm. Gradients are only read. Steps of one
+ * list change its tensors and must not run at once; otherwise a list is only
+ * read, from any stream and replayed graph. May be recorded into a HIP graph.
  * Errors: DDP_ERR_INVALID (args out of the ranges above, a device scalar that
  * is misaligned or lies where the step writes, another device current than
  * the list's, a stream of another device), DDP_ERR_HIP. */
